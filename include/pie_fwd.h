@@ -401,6 +401,107 @@ int pie_fwd_set_timing_events(void* start_event, void* stop_event);
  * Errors: PIE_EINVAL for stage < -1, or stage >= 0 with wait_us == 0. */
 int pie_fwd_test_wait_expiry(int32_t stage, uint32_t wait_us);
 
+/* ---- caches of 8 bits, sliding windows, page copies ------------------------
+ * The Pie pages keep quantization and kernel choice behind the inference layer
+ * and express a sliding window as a mask; these calls are this library's forms
+ * of both for the cache itself.  A plan made with pie_fwd_cache_plan serves
+ *   - a cache of the pass dtype (PIE_KV_DTYPE): pie_fwd_append_kv,
+ *     pie_fwd_set_mask, pie_fwd_attend as for pie_fwd_plan, with the window
+ *     applied when there is one;
+ *   - a cache of 8-bit codes (PIE_KV_E4M3): pie_fwd_append_kv8 and
+ *     pie_fwd_attend_kv8 (the calls for the other kind are refused).
+ * pie_fwd_fold and pie_fwd_plan_destroy serve both. */
+#define PIE_KV_DTYPE 0 /* pools hold elements of the pass dtype                 */
+#define PIE_KV_E4M3 1  /* pools hold e4m3 codes, one scale per (page, kv head)  */
+typedef struct pie_fwd_cache {
+  int32_t kv_type; /* PIE_KV_*                                                  */
+  int32_t window;  /* 0: none.  Else a row at slot t sees slots s <= t, s <     */
+                   /*   kv_len with s > t - window or s < sinks                 */
+  int32_t sinks;   /* first slots of every lane that stay visible (0: none)     */
+} pie_fwd_cache;
+
+/* pie_fwd_workspace_bytes and pie_fwd_plan for a cache (NULL: the pass dtype,
+ * no window).  A windowed pass reads, per row block, the pages of the sinks
+ * and those from the first row's window on; pages in between are never read,
+ * so their page-table entries may name any page of the pool.
+ * Errors beside pie_fwd_plan's: PIE_EINVAL for an unknown kv_type, sinks
+ * without a window, a window together with a mask, or (PIE_KV_E4M3) two
+ * page-table entries of the pass that write one physical page (its slots share
+ * a scale); PIE_ERANGE for a negative window or sinks. */
+int pie_fwd_cache_workspace_bytes(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
+                                  const pie_fwd_meta* meta, size_t* bytes);
+int pie_fwd_cache_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
+                       const pie_fwd_meta* meta, void* dev_workspace, size_t ws_bytes,
+                       void* stream, pie_fwd_plan_t** out);
+
+/* pie_fwd_append_kv into a cache of 8-bit codes.
+ *   k_pool, v_pool: device [num_pool_pages][Hkv][P][d] bytes, e4m3 codes;
+ *   k_scale, v_scale: device [num_pool_pages][Hkv] bytes, E8M0: every slot of
+ *            page p and kv head g stands for code * 2^(scale[p][g] - 127).
+ * RoPE as in pie_fwd_append_kv, but with the angle exact to about 2^-53 turns
+ * per position at any position (the fp32 angle is off by 2^-9 rad at 32,768).
+ * For every page that rows of the pass write, and each of K and V and kv head:
+ *   need = the smallest e in [-40, 60] with max |x| <= 448 * 2^e over the
+ *          pass's new rows of that page (NaN aside);
+ *   live = the page's slots below max(kv_len, frozen_len) that the pass does
+ *          not write;
+ *   e'   = need when no slot is live, else max(need, the page's e);
+ *   live codes become the nearest e4m3 of code * 2^(e - e'), new ones the
+ *   nearest e4m3 of x / 2^e' (ties to even, saturating at 448; NaN stays NaN).
+ * Power-of-two scales cost e4m3, a floating format, no precision, and a page
+ * that grows keeps its codes' significands.  The nearest code is that of the
+ * exact rotation.  Slots that are neither live nor written keep their codes.
+ * Frozen slots are not written (PIE_STATUS_FROZEN_WRITE), as in
+ * pie_fwd_append_kv; they stay live.  The fold checks are the same.
+ * Errors: PIE_EINVAL for a NULL required pointer, one off a 16-byte boundary
+ * (scales, frozen_len and status aside), or a plan of another cache. */
+int pie_fwd_append_kv8(const pie_fwd_plan_t* plan, const void* q, const void* k, const void* v,
+                       void* q_rot, uint8_t* k_pool, uint8_t* v_pool, uint8_t* k_scale,
+                       uint8_t* v_scale, const int32_t* frozen_len, uint32_t* status,
+                       void* stream);
+
+/* pie_fwd_attend over a cache of 8-bit codes: the same outputs, for the values
+ * the codes stand for.  With mask words, 64-slot tiles that no row of an item
+ * sees are not read; pie_fwd_set_mask has nothing to prepare.
+ * Precondition: scales of pages read are in [87, 187] (2^-40 .. 2^60, what
+ * pie_fwd_append_kv8 writes) and slots below kv_len hold no NaN code.
+ * Products are exact in fp16 operands (query vectors scaled to fp16's range by
+ * a power of two, fp32 ones split in two halves), sums fp32; the softmax
+ * weights enter the second product rounded to fp16 (in two halves for fp32).
+ * Calls on one plan share its workspace and are queued one after another. */
+int pie_fwd_attend_kv8(const pie_fwd_plan_t* plan, const void* q_rot, const uint8_t* k_pool,
+                       const uint8_t* v_pool, const uint8_t* k_scale, const uint8_t* v_scale,
+                       const uint32_t* mask_words, void* out_readout, float* lse_readout,
+                       void* out_all, float* lse_all, uint32_t* status, void* stream);
+
+/* pie_fwd_forward for a cache: plan, append, attend and fold of one pass
+ * (k_scale and v_scale are NULL for PIE_KV_DTYPE). */
+int pie_fwd_forward_cache(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
+                          const pie_fwd_meta* meta, void* dev_workspace, size_t ws_bytes,
+                          const void* q, const void* k, const void* v, void* q_rot, void* k_pool,
+                          void* v_pool, uint8_t* k_scale, uint8_t* v_scale, int32_t* frozen_len,
+                          const uint32_t* mask_words, void* out_readout, float* lse_readout,
+                          void* out_all, float* lse_all, const int32_t* channel,
+                          uint32_t* status, void* stream);
+
+/* Copy pages within pools: dst[i] becomes src[i] in every pool, as a fork does
+ * with its last, partly filled page before either branch writes it, or a
+ * compaction with the pages that move to the pool's front.  One launch per
+ * PIE_COPY_POOLS pools (all layers' K, V and scales of a model at once).
+ *   pools: HOST array of num_pools device addresses, page_bytes: HOST array of
+ *            each pool's bytes per page (any number; pools whose address and
+ *            page size are multiples of 16 move 16 bytes at a time);
+ *   src, dst: device int32 [num_pairs].  A pair with an id outside
+ *            [0, num_pool_pages) is skipped and sets PIE_STATUS_BOUNDS.  No
+ *            page may be the destination of two pairs, or a source of one and
+ *            the destination of another: their contents are then unspecified
+ *            (src[i] == dst[i] is allowed).
+ * Errors: PIE_EINVAL (negative counts, NULL required pointers, page_bytes < 1). */
+#define PIE_COPY_POOLS 128
+int pie_fwd_copy_pages(int32_t num_pools, void* const* pools, const int64_t* page_bytes,
+                       int32_t num_pool_pages, int32_t num_pairs, const int32_t* src,
+                       const int32_t* dst, uint32_t* status, void* stream);
+
 /* ABI version of this header (major * 100 + minor). */
 int pie_fwd_abi_version(void);
 

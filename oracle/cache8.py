@@ -1,0 +1,143 @@
+"""Plain 64-bit restatement of the cache operators beside the ForwardPass's own
+(TEST INFRASTRUCTURE ONLY): the append into a cache of 8-bit codes, attention
+over the values that codes or pools hold under a window, a mask or the default
+visibility, with the error bounds the tests derive from, and page copies.
+
+Everything is written row by row and slot by slot from the definitions in
+include/pie_fwd.h and shares no code with the library.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+MIN_EXP, MAX_EXP, BIAS, TOP = -40, 60, 127, 448.0
+
+
+def e4m3_table() -> np.ndarray:
+    """Value of each of the 256 codes (NaN for 0x7f and 0xff)."""
+    t = np.zeros(256)
+    for c in range(128):
+        e, m = c >> 3, c & 7
+        t[c] = m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)
+    t[127] = np.nan
+    t[128:] = -t[:128]
+    return t
+
+
+TABLE = e4m3_table()
+_POS = TABLE[:127]
+
+
+def encode(x: np.ndarray) -> np.ndarray:
+    """Codes of the nearest e4m3 values (the even code at a tie), saturating;
+    NaN becomes 0x7f."""
+    x = np.asarray(x, np.float64)
+    a = np.minimum(np.abs(np.nan_to_num(x, nan=0.0, posinf=1e300, neginf=-1e300)), TOP)
+    hi = np.minimum(np.searchsorted(_POS, a), 126)
+    lo = np.maximum(hi - 1, 0)
+    up, down = _POS[hi] - a, a - _POS[lo]
+    pick = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    pick = np.where(np.signbit(x), pick + 128, pick)
+    return np.where(np.isnan(x), 127, pick).astype(np.uint8)
+
+
+def rope(x: np.ndarray, positions: np.ndarray, base: float) -> np.ndarray:
+    """[N, H, d] rotated at the rows' positions, in float64."""
+    h = x.shape[-1] // 2
+    f = float(base) ** (-2.0 * np.arange(h) / x.shape[-1])
+    a = np.asarray(positions, np.float64)[:, None, None] * f
+    lo, hi = x[..., :h].astype(np.float64), x[..., h:].astype(np.float64)
+    return np.concatenate([lo * np.cos(a) - hi * np.sin(a), hi * np.cos(a) + lo * np.sin(a)], -1)
+
+
+def needed_exp(amax: float) -> int:
+    e = MIN_EXP
+    while e < MAX_EXP and amax > TOP * 2.0 ** e:
+        e += 1
+    return e
+
+
+def append(desc, p, x_new: np.ndarray, codes: np.ndarray, scale: np.ndarray, frozen) -> None:
+    """Write the rows' x_new [N, Hkv, d] (K already rotated, or V) into codes
+    [pages, Hkv, P, d] and scale [pages, Hkv], in place."""
+    P = desc.page_size
+    for l in range(len(p.kv_len)):
+        r0, r1 = int(p.row_indptr[l]), int(p.row_indptr[l + 1])
+        rows = [r for r in range(r0, r1) if p.slots[r] >= frozen[l]]
+        for lp in sorted({int(p.slots[r]) // P for r in rows}):
+            page = int(p.page_ids[p.page_indptr[l] + lp])
+            mine = [r for r in rows if p.slots[r] // P == lp]
+            offs = [int(p.slots[r]) % P for r in mine]
+            live = [o for o in range(P)
+                    if lp * P + o < max(int(p.kv_len[l]), int(frozen[l])) and o not in offs]
+            for g in range(desc.num_kv_heads):
+                mag = np.abs(x_new[mine, g])
+                mag = mag[~np.isnan(mag)]
+                e = needed_exp(mag.max() if mag.size else 0.0)
+                old = int(scale[page, g]) - BIAS
+                if live:
+                    e = max(e, old)
+                    if e != old:
+                        codes[page, g, live] = encode(TABLE[codes[page, g, live]] * 2.0 ** (old - e))
+                codes[page, g, offs] = encode(x_new[mine, g] / 2.0 ** e)
+                scale[page, g] = e + BIAS
+
+
+def values(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:
+    return TABLE[codes] * 2.0 ** (scale.astype(np.float64) - BIAS)[:, :, None, None]
+
+
+def visible(p, l: int, r: int, window: int = 0, sinks: int = 0) -> np.ndarray:
+    """Slots of lane l that row r sees."""
+    s = np.arange(int(p.kv_len[l]))
+    if p.mask_words is not None:
+        w = p.mask_words[p.mask_word_indptr[r]:p.mask_word_indptr[r + 1]]
+        return s[(w[s >> 5] >> (s & 31).astype(np.uint32)) & 1 == 1]
+    t = int(p.slots[r])
+    s = s[s <= t]
+    return s[(s > t - window) | (s < sinks)] if window else s
+
+
+def attend(desc, p, q_rot, k_val, v_val, window=0, sinks=0, weight_bits=11, weight_floor=0.0,
+           query_eps=0.0, v_scale=None):
+    """(out [N, Hq, d], lse [N, Hq], out_tol, lse_tol) in float64.
+
+    The tolerances bound a kernel that takes exact products of the operands,
+    sums in fp32 and rounds the softmax weights to `weight_bits` bits:
+      * a score's error is at most E = ((d + 4) 2^-24 + query_eps) sm <|q|, |k|>
+        (d products and the scale, each a half step of fp32, in any order);
+      * a weight then carries 2 E (its own and, through the sum, the others'),
+        2^-weight_bits, 2^-21 for the exponential and the exponent's rounding,
+        and sums of n terms n 2^-24;
+      * weights below the narrow format's range are off by at most
+        weight_floor of the largest weight times its V scale (v_scale per
+        slot), times the largest code, 448, for each of n slots.
+    Rounding the output to its type is added by the caller."""
+    Hq, Hkv, d, P = desc.num_q_heads, desc.num_kv_heads, desc.head_dim, desc.page_size
+    G = Hq // Hkv
+    sm = desc.sm_scale or 1.0 / np.sqrt(d)
+    N = len(p.slots)
+    out, lse = np.zeros((N, Hq, d)), np.full((N, Hq), -np.inf)
+    otol, ltol = np.zeros((N, Hq, d)), np.zeros((N, Hq))
+    for l in range(len(p.kv_len)):
+        ids = p.page_ids[p.page_indptr[l]:p.page_indptr[l + 1]]
+        for r in range(int(p.row_indptr[l]), int(p.row_indptr[l + 1])):
+            s = visible(p, l, r, window, sinks)
+            if s.size == 0:
+                continue
+            page, off = ids[s // P], s % P
+            for h in range(Hq):
+                k, v = k_val[page, h // G, off], v_val[page, h // G, off]
+                z = sm * (k @ q_rot[r, h])
+                E = ((d + 4) * 2.0 ** -24 + query_eps) * sm * (np.abs(k) @ np.abs(q_rot[r, h])).max()
+                w = np.exp(z - z.max())
+                tot = w.sum()
+                out[r, h] = w @ v / tot
+                lse[r, h] = z.max() + np.log(tot)
+                rel = 2 * E + 2.0 ** -weight_bits + 2.0 ** -21 + s.size * 2.0 ** -24
+                otol[r, h] = rel * (w @ np.abs(v)) / tot
+                if weight_floor:
+                    sv = v_scale[page, h // G]
+                    otol[r, h] += weight_floor * s.size * 448.0 * (w * sv).max() / tot
+                ltol[r, h] = E + 2.0 ** -21 + s.size * 2.0 ** -24 + 2.0 ** -22 * (abs(lse[r, h]) + 64)
+    return out, lse, otol, ltol

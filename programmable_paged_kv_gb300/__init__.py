@@ -17,13 +17,15 @@ import numpy as np
 
 from . import abi
 from .abi import (PIE_BF16, PIE_F32, PIE_FOLD_ALL, PIE_FOLD_CHANNEL, PIE_FOLD_COUNT,
-                  PIE_FOLD_NONE, PIE_STATUS_FOLD_CLAMP, PIE_STATUS_FOLD_GAP,
+                  PIE_FOLD_NONE, PIE_KV_DTYPE, PIE_KV_E4M3, PIE_STATUS_BOUNDS,
+                  PIE_STATUS_FOLD_CLAMP, PIE_STATUS_FOLD_GAP,
                   PIE_STATUS_FROZEN_WRITE, PIE_STATUS_TIMEOUT, PieError)
 
 __all__ = ["ForwardPlan", "PieError", "make_desc", "make_meta", "workspace_bytes", "build",
            "set_timing_events", "readout_topk", "readout_topk_workspace_bytes",
            "decode_loop", "decode_loop_workspace_bytes", "AdapterPlan", "adapter_workspace_bytes",
-           "Batcher",
+           "Batcher", "make_cache", "forward_cache", "copy_pages", "PIE_KV_DTYPE", "PIE_KV_E4M3",
+           "PIE_STATUS_BOUNDS",
            "PIE_F32", "PIE_BF16", "PIE_FOLD_NONE", "PIE_FOLD_ALL", "PIE_FOLD_COUNT",
            "PIE_FOLD_CHANNEL", "PIE_STATUS_FROZEN_WRITE", "PIE_STATUS_FOLD_CLAMP",
            "PIE_STATUS_FOLD_GAP", "PIE_STATUS_TIMEOUT"]
@@ -74,10 +76,22 @@ def make_meta(p, num_pool_pages: int, page_ids=None) -> _HostMeta:
                      p.fold_count, p.mask_word_indptr, p.readout)
 
 
-def workspace_bytes(desc: abi.pie_fwd_desc, meta: _HostMeta) -> int:
+def make_cache(kv: Optional[str] = None, window: int = 0, sinks: int = 0) -> abi.pie_fwd_cache:
+    """The cache a plan serves: kv None (pools of the pass dtype) or "e4m3" (8-bit
+    codes with a power-of-two scale per page and kv head); window: 0, or the
+    slots a row sees up to and with its own; sinks: first slots of a lane that
+    stay visible beside the window."""
+    if kv not in (None, "e4m3"):
+        raise ValueError(f"kv must be None or 'e4m3', not {kv!r}")
+    return abi.pie_fwd_cache(PIE_KV_DTYPE if kv is None else PIE_KV_E4M3, int(window), int(sinks))
+
+
+def workspace_bytes(desc: abi.pie_fwd_desc, meta: _HostMeta,
+                    cache: Optional[abi.pie_fwd_cache] = None) -> int:
     n = C.c_size_t(0)
-    abi.check(abi.load().pie_fwd_workspace_bytes(C.byref(desc), C.byref(meta.c), C.byref(n)),
-              "pie_fwd_workspace_bytes")
+    abi.check(abi.load().pie_fwd_cache_workspace_bytes(
+        C.byref(desc), None if cache is None else C.byref(cache), C.byref(meta.c), C.byref(n)),
+        "pie_fwd_workspace_bytes")
     return int(n.value)
 
 
@@ -108,6 +122,64 @@ def forward(desc: abi.pie_fwd_desc, meta: _HostMeta, workspace, q, k, v, q_rot, 
         _ptr(lse_readout, "lse_readout", False), _ptr(out_all, "out_all", False),
         _ptr(lse_all, "lse_all", False), _ptr(channel, "channel", False),
         _ptr(status, "status", False), _stream(stream)), "pie_fwd_forward")
+
+
+def forward_cache(desc: abi.pie_fwd_desc, cache: abi.pie_fwd_cache, meta: _HostMeta, workspace, q,
+                  k, v, q_rot, k_pool, v_pool, frozen_len, k_scale=None, v_scale=None,
+                  mask_words=None, out_readout=None, lse_readout=None, out_all=None, lse_all=None,
+                  channel=None, status=None, stream=None) -> None:
+    """pie_fwd_forward_cache: plan, append, attend and fold of one pass on the
+    given cache in one native call; k_scale and v_scale belong to an e4m3
+    cache.  workspace: as in forward(), sized by workspace_bytes(desc, meta,
+    cache)."""
+    if cache.kv_type == PIE_KV_E4M3:
+        _check_kv8(desc, k_pool, v_pool, k_scale, v_scale, int(meta.c.num_pool_pages))
+    dt = _torch_dtype(desc)
+    rows = _check_rows(desc, int(meta.c.num_rows), q=q, q_rot=q_rot, out_all=out_all)
+    _check_kv_rows(desc, rows, k=k, v=v)
+    _same_device(workspace, q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale, frozen_len,
+                 mask_words, out_readout, lse_readout, out_all, lse_all, channel, status)
+    if out_readout is not None and out_readout.dtype != dt:
+        raise ValueError(f"out_readout must be {dt}")
+    abi.check(abi.load().pie_fwd_forward_cache(
+        C.byref(desc), C.byref(cache), C.byref(meta.c), _ptr(workspace, "workspace"),
+        workspace.numel(), _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(q_rot, "q_rot"),
+        _ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"), _ptr(k_scale, "k_scale", False),
+        _ptr(v_scale, "v_scale", False), _ptr(frozen_len, "frozen_len"),
+        _ptr(mask_words, "mask_words", False), _ptr(out_readout, "out_readout", False),
+        _ptr(lse_readout, "lse_readout", False), _ptr(out_all, "out_all", False),
+        _ptr(lse_all, "lse_all", False), _ptr(channel, "channel", False),
+        _ptr(status, "status", False), _stream(stream)), "pie_fwd_forward_cache")
+
+
+def copy_pages(pools, src, dst, status=None, stream=None) -> None:
+    """pie_fwd_copy_pages: page dst[i] becomes page src[i] in each of `pools`
+    (contiguous CUDA tensors of any dtypes whose first dimension counts the
+    same pages: the K, V and scale pools of a model's layers); src and dst are
+    int32 CUDA tensors of one length."""
+    import torch
+    pools = list(pools)
+    if not pools:
+        return
+    pages = int(pools[0].shape[0])
+    for t in pools:
+        if t.dim() < 1 or int(t.shape[0]) != pages:
+            raise ValueError("the pools must have the same number of pages")
+    for t, what in ((src, "src"), (dst, "dst")):
+        if t.dtype != torch.int32 or t.dim() != 1:
+            raise ValueError(f"{what} must be a 1-D int32 tensor")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have one length")
+    _same_device(src, dst, status, *pools)
+    if pages == 0 or src.numel() == 0:
+        return
+    keep = [t for t in pools if t.numel()]
+    n = len(keep)
+    ptrs = (C.c_void_p * max(n, 1))(*[_ptr(t, "pool") for t in keep])
+    size = (C.c_int64 * max(n, 1))(*[t.numel() // pages * t.element_size() for t in keep])
+    abi.check(abi.load().pie_fwd_copy_pages(n, ptrs, size, pages, src.numel(), _ptr(src, "src"),
+                                            _ptr(dst, "dst"), _ptr(status, "status", False),
+                                            _stream(stream)), "pie_fwd_copy_pages")
 
 
 def decode_loop_workspace_bytes(desc: abi.pie_fwd_desc, num_lanes: int, max_pages_per_lane: int) -> int:
@@ -178,6 +250,45 @@ def _ptr(t, what: str, required: bool = True):
     return t.data_ptr()
 
 
+def _same_device(*tensors) -> None:
+    """Every tensor given lives on the current device (the launches go there)."""
+    import torch
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != here):
+            raise ValueError("every tensor must be on the current CUDA device")
+
+
+def _torch_dtype(desc):
+    import torch
+    return torch.bfloat16 if desc.dtype == PIE_BF16 else torch.float32
+
+
+def _check_rows(desc, rows: int, **tensors) -> int:
+    """Query-shaped tensors: [rows, num_q_heads, head_dim] of the pass dtype."""
+    want = (rows, desc.num_q_heads, desc.head_dim)
+    for what, t in tensors.items():
+        if t is not None and (tuple(t.shape) != want or t.dtype != _torch_dtype(desc)):
+            raise ValueError(f"{what} must be {want} of {_torch_dtype(desc)}")
+    return rows
+
+
+def _check_kv_rows(desc, rows: int, **tensors) -> None:
+    want = (rows, desc.num_kv_heads, desc.head_dim)
+    for what, t in tensors.items():
+        if tuple(t.shape) != want or t.dtype != _torch_dtype(desc):
+            raise ValueError(f"{what} must be {want} of {_torch_dtype(desc)}")
+
+
+def _check_kv8(desc, k_pool, v_pool, k_scale, v_scale, pages: int) -> None:
+    """Pools of codes [pages, Hkv, P, d] and scales [pages, Hkv], one byte each."""
+    shape = (pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
+    for what, t, want in (("k_pool", k_pool, shape), ("v_pool", v_pool, shape),
+                          ("k_scale", k_scale, shape[:2]), ("v_scale", v_scale, shape[:2])):
+        if t is None or tuple(t.shape) != want or t.element_size() != 1:
+            raise ValueError(f"{what} must be {want} of one byte each")
+
+
 def _stream(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -189,24 +300,28 @@ class ForwardPlan:
 
     desc: pie_fwd_desc (see make_desc); meta: _HostMeta (see make_meta).
     workspace: optional uint8 CUDA tensor of at least workspace_bytes();
-    allocated here when omitted.
+    allocated here when omitted.  cache: optional pie_fwd_cache (see
+    make_cache); a plan for an e4m3 cache has append_kv8 and attend_kv8 in the
+    place of append_kv and attend.
     """
 
-    def __init__(self, desc: abi.pie_fwd_desc, meta: _HostMeta, workspace=None, stream=None):
+    def __init__(self, desc: abi.pie_fwd_desc, meta: _HostMeta, workspace=None, stream=None,
+                 cache: Optional[abi.pie_fwd_cache] = None):
         import torch
         self.lib = abi.load()
         self.desc = desc
         self.meta = meta
         if workspace is None:
-            need = workspace_bytes(desc, meta)
+            need = workspace_bytes(desc, meta, cache)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
         # a caller-supplied workspace that is too small is refused by the
         # planner itself (PIE_ENOSPACE)
         self.workspace = workspace
         h = C.c_void_p()
-        abi.check(self.lib.pie_fwd_plan(C.byref(desc), C.byref(meta.c), _ptr(workspace, "workspace"),
-                                        workspace.numel(), _stream(stream), C.byref(h)),
-                  "pie_fwd_plan")
+        abi.check(self.lib.pie_fwd_cache_plan(
+            C.byref(desc), None if cache is None else C.byref(cache), C.byref(meta.c),
+            _ptr(workspace, "workspace"), workspace.numel(), _stream(stream), C.byref(h)),
+            "pie_fwd_plan")
         self.handle = h
         self.num_readout = int(self.lib.pie_fwd_plan_num_readout(h))
 
@@ -243,6 +358,37 @@ class ForwardPlan:
             _ptr(lse_readout, "lse_readout", False), _ptr(out_all, "out_all", False),
             _ptr(lse_all, "lse_all", False), _ptr(status, "status", False), _stream(stream)),
             "pie_fwd_attend")
+
+    def append_kv8(self, q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale, frozen_len, status=None,
+                   stream=None):
+        """pie_fwd_append_kv8: k_pool / v_pool [pages, Hkv, P, d] e4m3 codes (any
+        1-byte dtype), k_scale / v_scale [pages, Hkv] E8M0 bytes."""
+        rows = _check_rows(self.desc, int(self.meta.c.num_rows), q=q, q_rot=q_rot)
+        _check_kv_rows(self.desc, rows, k=k, v=v)
+        _check_kv8(self.desc, k_pool, v_pool, k_scale, v_scale, int(self.meta.c.num_pool_pages))
+        _same_device(q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale, frozen_len, status)
+        abi.check(self.lib.pie_fwd_append_kv8(
+            self.handle, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(q_rot, "q_rot"),
+            _ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"), _ptr(k_scale, "k_scale"),
+            _ptr(v_scale, "v_scale"), _ptr(frozen_len, "frozen_len"),
+            _ptr(status, "status", False), _stream(stream)), "pie_fwd_append_kv8")
+
+    def attend_kv8(self, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words=None,
+                   out_readout=None, lse_readout=None, out_all=None, lse_all=None, status=None,
+                   stream=None):
+        """pie_fwd_attend_kv8: attend() over the codes and scales of append_kv8."""
+        rows = _check_rows(self.desc, int(self.meta.c.num_rows), q_rot=q_rot, out_all=out_all)
+        _check_rows(self.desc, self.num_readout, out_readout=out_readout)
+        _check_kv8(self.desc, k_pool, v_pool, k_scale, v_scale, int(self.meta.c.num_pool_pages))
+        _same_device(q_rot, k_pool, v_pool, k_scale, v_scale, mask_words, out_readout, lse_readout,
+                     out_all, lse_all, status)
+        abi.check(self.lib.pie_fwd_attend_kv8(
+            self.handle, _ptr(q_rot, "q_rot"), _ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"),
+            _ptr(k_scale, "k_scale"), _ptr(v_scale, "v_scale"),
+            _ptr(mask_words, "mask_words", False), _ptr(out_readout, "out_readout", False),
+            _ptr(lse_readout, "lse_readout", False), _ptr(out_all, "out_all", False),
+            _ptr(lse_all, "lse_all", False), _ptr(status, "status", False), _stream(stream)),
+            "pie_fwd_attend_kv8")
 
     def fold(self, frozen_len, channel=None, status=None, stream=None):
         abi.check(self.lib.pie_fwd_fold(

@@ -25,6 +25,9 @@ PIE_EUNSUPPORTED = -5
 PIE_F32 = 0
 PIE_BF16 = 1
 
+PIE_KV_DTYPE = 0
+PIE_KV_E4M3 = 1
+
 PIE_FOLD_NONE = 0
 PIE_FOLD_ALL = 1
 PIE_FOLD_COUNT = 2
@@ -32,6 +35,7 @@ PIE_FOLD_CHANNEL = 3
 
 PIE_STATUS_FROZEN_WRITE = 1
 PIE_STATUS_FOLD_CLAMP = 2
+PIE_STATUS_BOUNDS = 4
 PIE_STATUS_FOLD_GAP = 8
 PIE_STATUS_TIMEOUT = 16
 PIE_STATUS_NOALLOC_TRUNC = 32
@@ -42,6 +46,10 @@ class pie_fwd_desc(C.Structure):
     _fields_ = [("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32),
                 ("head_dim", C.c_int32), ("page_size", C.c_int32), ("dtype", C.c_int32),
                 ("rope_base", C.c_float), ("sm_scale", C.c_float)]
+
+
+class pie_fwd_cache(C.Structure):
+    _fields_ = [("kv_type", C.c_int32), ("window", C.c_int32), ("sinks", C.c_int32)]
 
 
 class pie_fwd_meta(C.Structure):
@@ -89,6 +97,12 @@ SIGNATURES = {
                                                 _P, _P, _P, _P, C.c_int32, _P, _P, _P, _P, _P,
                                                 _P, _P]),
     "pie_fwd_test_wait_expiry": (C.c_int, [C.c_int32, C.c_uint32]),
+    "pie_fwd_cache_workspace_bytes": (C.c_int, [_P, _P, _P, C.POINTER(C.c_size_t)]),
+    "pie_fwd_cache_plan": (C.c_int, [_P, _P, _P, _P, C.c_size_t, _P, C.POINTER(_P)]),
+    "pie_fwd_append_kv8": (C.c_int, [_P] * 12),
+    "pie_fwd_attend_kv8": (C.c_int, [_P] * 13),
+    "pie_fwd_forward_cache": (C.c_int, [_P, _P, _P, _P, C.c_size_t] + [_P] * 17),
+    "pie_fwd_copy_pages": (C.c_int, [C.c_int32, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P]),
     "pie_fwd_adapter_workspace_bytes": (C.c_int, [C.c_int32, _P, C.c_int32,
                                                   C.POINTER(C.c_size_t)]),
     "pie_fwd_adapter_plan": (C.c_int, [C.c_int32, _P, _P, C.c_int32, C.c_int32, _P, C.c_size_t,

@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(DecCfg<T, D, NQ>::THREADS, DecCfg<T, D, NQ>::M
   const int kb = it.kv_begin, ke = it.kv_end;
   const int nstages = ke > kb ? (ke - kb + kStageSlots - 1) / kStageSlots : 0;
   const int nqv = it.nrows * G;  // valid query vectors
+  const int skip = window_pages(it.block);
+  const WindowView view(m, P, skip);
 
   // every wait gives up after the limit (the test hook may shorten it)
   const uint64_t wait_ns = m.test_wait_us ? uint64_t(m.test_wait_us) * 1000ull : kWaitLimitNs;
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(DecCfg<T, D, NQ>::THREADS, DecCfg<T, D, NQ>::M
     auto page_of = [&](int s) -> int64_t {
       const int sb = kb + s * kStageSlots;
       const int p0 = sb / P, p1 = (min(sb + kStageSlots, ke) - 1) / P;
-      return (lane >> 1) <= p1 - p0 ? int64_t(pages[p0 + (lane >> 1)]) : 0;
+      const int pg = p0 + (lane >> 1);
+      return (lane >> 1) <= p1 - p0 ? int64_t(pages[pg + (pg >= m.sink_pages ? skip : 0)]) : 0;
     };
     int64_t pid = nstages > 0 ? page_of(0) : 0;
     for (int s = 0; s < nstages; ++s) {
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, NQ>::THREADS, DecCfg<T, D, NQ>::M
       for (int e = 0; e < C::E; ++e) {
         const bool in = qvalid[e] && s_in_unit < nvalid;
         const bool vis = in && (mask_words ? ((word[e] >> (s_abs & 31)) & 1u) != 0
-                                           : s_abs <= slot_lim[e]);
+                                           : view.sees(slot_lim[e], view.slot(s_abs)));
         const float sc = vis ? part[e] : -INFINITY;
         const float m_new = fmaxf(m_run[e], warp_max_pairs(sc));
         const bool none = m_new == -INFINITY;

@@ -32,6 +32,9 @@
 // listed rows of a scattered list four at a time (tile::gather4 over one-row
 // boxes), and the rows' visibility comes from their mask words re-expressed
 // over the list.
+// In a windowed pass (WIN) an item's positions run over the row block's sink
+// pages and then its window's pages; the producer skips the pages between them
+// and every score is tested against its row's window and the sinks.
 // Each work item writes one partial (max, sum, unnormalised output) per query
 // vector; the combine kernel (combine.cu) merges an item's chunks.  Every wait
 // is bounded in time.
@@ -106,7 +109,7 @@ struct DecRange {
   bool listed, page_list, skip;  // skip: a listed chunk past the list's share
 };
 
-template <int NQ>
+template <int NQ, bool WIN>
 __global__ void __launch_bounds__(dm::THREADS, 3) attend_decode_mma_kernel(
     DevMeta m, int Hq, int Hkv, int G, int P, float scale_log2, const __nv_bfloat16* q_rot,
     const uint32_t* mask_words, int list_tile, int num_items, int items_per_cta,
@@ -239,6 +242,10 @@ __global__ void __launch_bounds__(dm::THREADS, 3) attend_decode_mma_kernel(
         const int sb = r.kb + s * kStageSlots;
         const int p0 = sb / P, p1 = (min(sb + kStageSlots, r.ke) - 1) / P;
         if (pi > p1 - p0) return 0;
+        if (WIN) {
+          const int pg = p0 + pi;
+          return int64_t(pages[pg + (pg >= m.sink_pages ? window_pages(r.it.block) : 0)]);
+        }
         return r.listed ? int64_t(lrow[(p0 + pi) * P]) / (int64_t(Hkv) * P)
                         : int64_t(pages[p0 + pi]);
       };
@@ -341,6 +348,7 @@ __global__ void __launch_bounds__(dm::THREADS, 3) attend_decode_mma_kernel(
     const DecItem& it = r.it;
     const int kb = r.kb, ke = r.ke, nstages = r.nstages;
     const int nqv = it.nrows * G;
+    const WindowView view(m, P, WIN ? window_pages(it.block) : 0);
     // the query vectors into shared memory (zeros past the item's), 16 bytes
     // per thread, chunks XOR-swizzled by the row so that ldmatrix reads of
     // the eight rows hit distinct banks; the B fragments of Q^T are read from
@@ -438,7 +446,9 @@ __global__ void __launch_bounds__(dm::THREADS, 3) attend_decode_mma_kernel(
         for (int e = 0; e < 4; ++e) {
           const int cs = g + 8 * (e >> 1), i = e & 1;
           const bool vis = valid_q[i] && cs < nvalid &&
-                           (mrow[i] ? ((word[i] >> cs) & 1u) != 0 : unit_base + cs <= slot_lim[i]);
+                           (WIN       ? view.sees(slot_lim[i], view.slot(unit_base + cs))
+                            : mrow[i] ? ((word[i] >> cs) & 1u) != 0
+                                      : unit_base + cs <= slot_lim[i]);
           cc[e] = vis ? cc[e] : -INFINITY;
         }
         float mt[2] = {fmaxf(cc[0], cc[2]), fmaxf(cc[1], cc[3])};
@@ -562,13 +572,13 @@ __global__ void __launch_bounds__(dm::THREADS, 3) attend_decode_mma_kernel(
   }
 }
 
-template <int NQ>
+template <int NQ, bool WIN>
 static cudaError_t launch_nq(const pie_fwd_plan_t& p, const void* q_rot,
                              const uint32_t* mask_words, uint32_t* status, const CUtensorMap& km,
                              const CUtensorMap& vm, const CUtensorMap& kgm, const CUtensorMap& vgm,
                              cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};  // per instantiation and device
-  cudaError_t e = set_smem_limit(attend_decode_mma_kernel<NQ>, dm::SMEM, configured);
+  cudaError_t e = set_smem_limit(attend_decode_mma_kernel<NQ, WIN>, dm::SMEM, configured);
   if (e != cudaSuccess) return e;
   DevMeta m = p.dev;
   test_wait_hook(&m.test_stall, &m.test_wait_us);
@@ -577,7 +587,7 @@ static cudaError_t launch_nq(const pie_fwd_plan_t& p, const void* q_rot,
   const int per = p.dec_items_per_cta > 0 ? p.dec_items_per_cta : 1;
   const int grid = p.dev.dec_work ? std::min(p.num_dec_items, 3 * std::max(1, p.dev.num_sms))
                                   : (p.num_dec_items + per - 1) / per;
-  return launch_dependent(attend_decode_mma_kernel<NQ>, dim3(grid), dim3(dm::THREADS),
+  return launch_dependent(attend_decode_mma_kernel<NQ, WIN>, dim3(grid), dim3(dm::THREADS),
                           dm::SMEM, s, true, m, p.desc.num_q_heads, p.desc.num_kv_heads, p.G,
                           p.desc.page_size, p.desc.sm_scale * dm::kLog2e,
                           static_cast<const __nv_bfloat16*>(q_rot), mask_words,
@@ -611,10 +621,17 @@ cudaError_t launch_attend_decode_mma(const pie_fwd_plan_t& p, const void* q_rot,
     if (!tc::make_map(&kgm, k_pool, 2, dims, str, box1)) return cudaErrorInvalidValue;
     if (!tc::make_map(&vgm, v_pool, 2, dims, str, box1)) return cudaErrorInvalidValue;
   }
+  if (p.dev.window > 0) {
+    switch (p.nq) {
+      case 2: return launch_nq<2, true>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
+      case 4: return launch_nq<4, true>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
+      default: return launch_nq<8, true>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
+    }
+  }
   switch (p.nq) {
-    case 2: return launch_nq<2>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
-    case 4: return launch_nq<4>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
-    default: return launch_nq<8>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
+    case 2: return launch_nq<2, false>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
+    case 4: return launch_nq<4, false>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
+    default: return launch_nq<8, false>(p, q_rot, mask_words, status, km, vm, kgm, vgm, s);
   }
 }
 

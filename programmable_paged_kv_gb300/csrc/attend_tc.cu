@@ -130,7 +130,7 @@ __device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t* r) {
 
 }  // namespace tc
 
-template <int NT>
+template <int NT, bool WIN>
 __global__ void __launch_bounds__(tc::Cfg<NT>::kThreads, 1) attend_tc_kernel(
     DevMeta m, int G, int Hq, int Hkv, int P, float scale_log2,
     const uint32_t* mask_words, tc::Out out, uint32_t* status,
@@ -255,7 +255,9 @@ __global__ void __launch_bounds__(tc::Cfg<NT>::kThreads, 1) attend_tc_kernel(
           const int p0 = ts / P, p1 = (te - 1) / P;
           if ((lane >> 1) <= p1 - p0)
             y[0][0] = page_list ? lrow[ts + (lane >> 1) * P] + hrow
-                                : (pages[p0 + (lane >> 1)] * Hkv + it.kv_head) * P;
+                                : (pages[WIN && p0 + (lane >> 1) >= m.sink_pages
+                                             ? p0 + (lane >> 1) + it.skip
+                                             : p0 + (lane >> 1)] * Hkv + it.kv_head) * P;
         }
       };
       coords(0);
@@ -390,6 +392,7 @@ __global__ void __launch_bounds__(tc::Cfg<NT>::kThreads, 1) attend_tc_kernel(
     if (masked && valid_q)
       mrow = gather ? m.cmask + mb.cmask_off + int64_t(row - mb.r0) * mb.nw
                     : mask_words + m.mask_word_indptr[row];
+    const WindowView view(m, P, WIN ? it.skip : 0);
     const uint32_t lane_base = tmem + (uint32_t(quad * 32) << 16);
     const uint32_t tO = lane_base + o_col(t);
     float m_used = -INFINITY, l_run = 0.f;
@@ -418,14 +421,23 @@ __global__ void __launch_bounds__(tc::Cfg<NT>::kThreads, 1) attend_tc_kernel(
         uint32_t wand = ~0u;
 #pragma unroll
         for (int i = 0; i < NW; ++i) wand &= words[i];
-        const bool all_vis = (ts + BN <= ke) &&
-                             (masked ? (wand == ~0u) : (ts + BN - 1 <= row_slot));
+        bool all_vis;
+        if constexpr (WIN) {
+          // the tile's slots follow one another unless it holds the end of the
+          // sink pages; then, or where its first slot lies before the row's
+          // window, its columns are tested one by one
+          const int s0 = view.slot(ts), s1 = view.slot(ts + BN - 1);
+          all_vis = ts + BN <= ke && s1 - s0 == BN - 1 && s1 <= row_slot && view.sees(row_slot, s0) &&
+                    (s0 > row_slot - view.window || s1 < view.sinks);
+        } else {
+          all_vis = (ts + BN <= ke) && (masked ? (wand == ~0u) : (ts + BN - 1 <= row_slot));
+        }
         if (!__all_sync(0xffffffffu, all_vis || !valid_q)) {
 #pragma unroll
           for (int c = 0; c < BN; ++c) {
             const int sa = ts + c;
             const bool vis = valid_q && sa < ke &&
-                             (masked ? ((words[c >> 5] >> (c & 31)) & 1u) != 0 : sa <= row_slot);
+                             (WIN ? view.sees(row_slot, view.slot(sa)) : masked ? ((words[c >> 5] >> (c & 31)) & 1u) != 0 : sa <= row_slot);
             s[c] = vis ? s[c] : -INFINITY;
           }
         }
@@ -549,16 +561,16 @@ __global__ void __launch_bounds__(tc::Cfg<NT>::kThreads, 1) attend_tc_kernel(
 // ---------------------------------------------------------------------------
 // host side: tensor maps and launch
 // ---------------------------------------------------------------------------
-template <int NT>
+template <int NT, bool WIN>
 static cudaError_t launch_nt(const pie_fwd_plan_t& p, const uint32_t* mask_words, tc::Out out,
                              uint32_t* status, const CUtensorMap& qm, const CUtensorMap& km,
                              const CUtensorMap& vm, const CUtensorMap& kgm,
                              const CUtensorMap& vgm, cudaStream_t s) {
   const size_t smem = sizeof(tc::Smem<NT>) + 1024;
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = set_smem_limit(attend_tc_kernel<NT>, int(smem), configured);
+  cudaError_t e = set_smem_limit(attend_tc_kernel<NT, WIN>, int(smem), configured);
   if (e != cudaSuccess) return e;
-  return launch_dependent(attend_tc_kernel<NT>, dim3(p.num_tc_items), dim3(tc::Cfg<NT>::kThreads),
+  return launch_dependent(attend_tc_kernel<NT, WIN>, dim3(p.num_tc_items), dim3(tc::Cfg<NT>::kThreads),
                           smem, s, true, p.dev, p.G, p.desc.num_q_heads, p.desc.num_kv_heads,
                           p.desc.page_size, p.desc.sm_scale * 1.4426950408889634f, mask_words, out,
                           status, qm, km, vm, kgm, vgm);
@@ -596,8 +608,11 @@ cudaError_t launch_attend_tc(const pie_fwd_plan_t& p, const void* q_rot, const v
   }
   tc::Out out{static_cast<__nv_bfloat16*>(out_readout), lse_readout,
               static_cast<__nv_bfloat16*>(out_all), lse_all};
-  return p.tc_nt == 2 ? launch_nt<2>(p, mask_words, out, status, qm, km, vm, kgm, vgm, s)
-                      : launch_nt<1>(p, mask_words, out, status, qm, km, vm, kgm, vgm, s);
+  if (p.dev.window > 0)
+    return p.tc_nt == 2 ? launch_nt<2, true>(p, mask_words, out, status, qm, km, vm, kgm, vgm, s)
+                        : launch_nt<1, true>(p, mask_words, out, status, qm, km, vm, kgm, vgm, s);
+  return p.tc_nt == 2 ? launch_nt<2, false>(p, mask_words, out, status, qm, km, vm, kgm, vgm, s)
+                      : launch_nt<1, false>(p, mask_words, out, status, qm, km, vm, kgm, vgm, s);
 }
 
 }  // namespace pie

@@ -265,6 +265,22 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1) 
       : "f"(a0), "f"(a1));
 }
 
+// A windowed pass's view of one row block (its items' positions count the slots
+// it reads; internal.h, window_pages): the lane's slot at a position, and
+// whether a row at slot t sees it.
+struct WindowView {
+  int window, sinks, sink_slots, skip_slots;
+  __device__ __forceinline__ WindowView(const DevMeta& m, int P, int skip_pages)
+      : window(m.window), sinks(m.sinks), sink_slots(m.sink_pages * P), skip_slots(skip_pages * P) {}
+  __device__ __forceinline__ int slot(int pos) const {
+    return pos + (pos >= sink_slots ? skip_slots : 0);
+  }
+  // (t - window does not overflow: t >= -1 and window > 0)
+  __device__ __forceinline__ bool sees(int t, int s) const {
+    return s <= t && (window == 0 || s > t - window || s < sinks);
+  }
+};
+
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);
 }

@@ -1,0 +1,114 @@
+// Page copies within the pools of a model's layers (a fork's last page, the
+// moves of a compaction): dst[i] <- src[i] in every pool, one launch for all
+// of them.
+//
+// Bound: HBM, every byte read once and written once.  Thread blocks walk
+// (pool, pair, part of a page) units of up to kUnit bytes; a thread keeps
+// kVec 16-byte loads in flight before it stores them.  Pools whose address or
+// page size is not a multiple of 16 (scale pools: a byte per kv head) are
+// copied by single bytes, a warp's worth of pairs at a time would cost more
+// than their few bytes.
+
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace pie {
+
+namespace cp {
+
+constexpr int THREADS = 256;
+constexpr int VEC = 4;                         // 16-byte vectors in flight per thread
+constexpr int UNIT = THREADS * VEC * 16;       // 16 KB
+
+struct Pools {
+  struct {
+    uint8_t* base;
+    int64_t page_bytes;
+  } pool[PIE_COPY_POOLS];
+};
+
+}  // namespace cp
+
+__global__ void __launch_bounds__(cp::THREADS) copy_pages_kernel(
+    const __grid_constant__ cp::Pools pools, int num_pool_pages, int num_pairs, const int32_t* src,
+    const int32_t* dst, uint32_t* status) {
+  using namespace cp;
+  grid_dep_wait();
+  grid_dep_launch();
+  uint8_t* base = pools.pool[blockIdx.y].base;
+  const int64_t bytes = pools.pool[blockIdx.y].page_bytes;
+  const bool wide = ((reinterpret_cast<uintptr_t>(base) | uint64_t(bytes)) & 15) == 0;
+  if (!wide) {
+    // one thread per byte of the pairs' pages
+    const int64_t total = bytes * num_pairs;
+    for (int64_t i = int64_t(blockIdx.x) * THREADS + threadIdx.x; i < total;
+         i += int64_t(gridDim.x) * THREADS) {
+      const int64_t pair = i / bytes;
+      const int s = src[pair], d = dst[pair];
+      if (uint32_t(s) >= uint32_t(num_pool_pages) || uint32_t(d) >= uint32_t(num_pool_pages)) {
+        set_status(status, PIE_STATUS_BOUNDS);
+        continue;
+      }
+      base[d * bytes + i % bytes] = base[s * bytes + i % bytes];
+    }
+    return;
+  }
+  const int64_t parts = (bytes + UNIT - 1) / UNIT;
+  const int64_t units = parts * num_pairs;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t pair = u / parts, part = u % parts;
+    const int s = src[pair], d = dst[pair];
+    if (uint32_t(s) >= uint32_t(num_pool_pages) || uint32_t(d) >= uint32_t(num_pool_pages)) {
+      if (threadIdx.x == 0) set_status(status, PIE_STATUS_BOUNDS);
+      continue;
+    }
+    const int64_t at = part * UNIT;
+    const int n = int(min(int64_t(UNIT), bytes - at) / 16);
+    const uint4* from = reinterpret_cast<const uint4*>(base + s * bytes + at);
+    uint4* to = reinterpret_cast<uint4*>(base + d * bytes + at);
+    uint4 v[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (int(threadIdx.x) + i * THREADS < n) v[i] = from[threadIdx.x + i * THREADS];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (int(threadIdx.x) + i * THREADS < n) to[threadIdx.x + i * THREADS] = v[i];
+  }
+}
+
+}  // namespace pie
+
+using namespace pie;
+
+extern "C" int pie_fwd_copy_pages(int32_t num_pools, void* const* pools, const int64_t* page_bytes,
+                                  int32_t num_pool_pages, int32_t num_pairs, const int32_t* src,
+                                  const int32_t* dst, uint32_t* status, void* stream) {
+  if (num_pools < 0 || num_pool_pages < 0 || num_pairs < 0)
+    return set_last_error(PIE_EINVAL, "copy_pages: negative count");
+  if (num_pools == 0 || num_pairs == 0) return PIE_OK;
+  if (!pools || !page_bytes || !src || !dst)
+    return set_last_error(PIE_EINVAL, "copy_pages: a required pointer is NULL");
+  for (int i = 0; i < num_pools; ++i) {
+    if (!pools[i]) return set_last_error(PIE_EINVAL, "copy_pages: a pool is NULL");
+    if (page_bytes[i] < 1) return set_last_error(PIE_EINVAL, "copy_pages: page_bytes must be positive");
+  }
+  const int waves = 8 * device_sm_count();  // thread blocks resident at once
+  for (int p0 = 0; p0 < num_pools; p0 += PIE_COPY_POOLS) {
+    const int n = std::min(PIE_COPY_POOLS, num_pools - p0);
+    cp::Pools arg = {};
+    int64_t units = 1;
+    for (int i = 0; i < n; ++i) {
+      arg.pool[i].base = static_cast<uint8_t*>(pools[p0 + i]);
+      arg.pool[i].page_bytes = page_bytes[p0 + i];
+      units = std::max<int64_t>(units, (page_bytes[p0 + i] + cp::UNIT - 1) / cp::UNIT * num_pairs);
+    }
+    const int gx = static_cast<int>(std::min<int64_t>(units, std::max(1, 2 * waves / n)));
+    cudaError_t e = launch_dependent(copy_pages_kernel, dim3(gx, n), dim3(cp::THREADS), 0,
+                                     static_cast<cudaStream_t>(stream), true, arg, num_pool_pages,
+                                     num_pairs, src, dst, status);
+    if (e != cudaSuccess)
+      return set_last_error(PIE_ECUDA, std::string("copy_pages launch: ") + cudaGetErrorString(e));
+  }
+  return PIE_OK;
+}

@@ -18,7 +18,10 @@ namespace pie {
 // partial slots part_base .. part_base + NQ - 1.  In masked passes `block` is
 // the row block whose compacted visible-slot list the item walks (else -1);
 // then kv_begin is the item's chunk and kv_end the chunks provisioned, and the
-// chunks used come from the list's length (masked_chunks).
+// chunks used come from the list's length (masked_chunks).  In windowed passes
+// kv_begin and kv_end count the slots the row block reads one after another --
+// the sink pages, then the pages from the window's first on -- and `block` is
+// -1 - (the pages left out between them); window_pages() below decodes it.
 struct alignas(16) DecItem {
   int32_t lane, kv_head, row0, nrows;
   int32_t kv_begin, kv_end, part_base, block;
@@ -37,6 +40,22 @@ constexpr int kDecListWaves = 6;
 // two consecutive items per CTA (masked decode 3-5 % faster than one; the
 // counter gave the same kernel times and slower calls).
 constexpr int kDecListItemsPerCta = 2;
+
+// The slots a row block of a windowed pass reads, in order: positions
+// [0, sink_pages * P) are the lane's own slots, later ones lie `skip` pages
+// further on.  A pass without a window has skip 0.
+__host__ __device__ inline int window_pages(int block) { return block < -1 ? -1 - block : 0; }
+
+// A page that rows of the pass write in a cache of 8-bit codes: the rows
+// wrow[row0 .. row0 + nrows) of `lane`, all in its page-table entry `lpage`,
+// whose physical page is `page`; bit o of `written` says a row writes slot
+// offset o.
+struct alignas(16) WriteBlock {
+  int32_t lane, lpage, page, row0;
+  int32_t nrows;
+  uint32_t written;
+  int32_t pad0, pad1;
+};
 
 // How the combine step finds the partials of a row block (the rows one work
 // item serves) and kv head: row r of the block, q head h, chunk c lives at
@@ -64,7 +83,8 @@ struct alignas(16) TcItem {
   // masked passes: the row block whose compacted visible-slot list the item
   // walks (else -1), and this item's share of it: chunk `chunk` of `nchunks`
   // equal shares of the list's 128-entry tiles (kv_begin/kv_end unused)
-  int32_t block, chunk, nchunks, pad;
+  int32_t block, chunk, nchunks;
+  int32_t skip;  // windowed passes: pages left out behind the sink pages
 };
 
 // A row block of a masked pass: rows [r0, r1) of
@@ -82,6 +102,7 @@ constexpr int kStageSlots = 64;   // slots per pipeline stage of the decode kern
 constexpr int kWarpSlots = 16;    // slots per compute warp per stage
 constexpr int kTcTileSlots = 128; // slots per KV tile of the tensor-core kernel
 constexpr int kTcTileQueries = 128;
+constexpr int kWideQueries = 32;  // query vectors per wide item of the 8-bit cache's kernel
 // SMs the tensor-core work is sized for when no device is visible (host-only
 // planning, e.g. pie_fwd_workspace_bytes on a machine without a GPU); with a
 // device, its multiprocessor count is used (device_sm_count).
@@ -124,6 +145,10 @@ struct DevMeta {
   const int32_t* ro_indptr;         // [N+1]: readout positions of row r are
   const int32_t* ro_idx;            //   ro_idx[ro_indptr[r] .. ro_indptr[r+1])
   const float* rope_freq;           // [d/2]
+  const uint64_t* rope_turn;        // [d/2] turns per position, 0.64 fixed point (8-bit caches)
+  const WriteBlock* wblocks;        // pages written (8-bit caches)
+  const int32_t* wrow;              // [N] rows in the order of the pages they write
+  const DecItem* wide_items;        // 8-bit caches: items of up to kWideQueries query vectors
   const DecItem* dec_items;
   const TcItem* tc_items;
   const CombEntry* comb;            // [row blocks * Hkv]
@@ -144,6 +169,9 @@ struct DevMeta {
                                     //   its fixed run of items
   int32_t num_sms;                  // SMs the masked units' chunks are sized for
   int32_t num_pool_pages;           // page ids at or past it are skipped (PIE_STATUS_BOUNDS)
+  int32_t window, sinks;            // row at slot t sees s > t - window or s < sinks
+                                    //   (window 0: every s <= t)
+  int32_t sink_pages;               // pages holding the sinks
   int32_t test_stall;               // test hook: 0 none; s + 1: the split-KV producer stops
                                     //   before stage s of every item
   uint32_t test_wait_us;            // test hook: 0, or the split-KV kernel's wait limit in us
@@ -187,6 +215,8 @@ struct pie_fwd_plan {
   int32_t mblock_max_rows;   // most rows in a masked row block
   int64_t num_part_slots;
   int32_t num_comb_merge;    // combine entries with chunks to merge (0: no combine launch)
+  bool kv8;                  // the pools hold 8-bit codes (pie_fwd_cache.kv_type)
+  int32_t num_wblocks, num_wide_items;
   const uint32_t* mask_set;  // mask words whose compacted lists the workspace holds
                              // (pie_fwd_set_mask), or NULL
   pie::DevMeta dev;
@@ -218,6 +248,14 @@ cudaError_t launch_attend_tc(const pie_fwd_plan_t& p, const void* q_rot, const v
                              cudaStream_t s);
 cudaError_t launch_mask_compact(const pie_fwd_plan_t& p, const uint32_t* mask_words,
                                 cudaStream_t s);
+cudaError_t launch_append_kv8(const pie_fwd_plan_t& p, const void* q, const void* k, const void* v,
+                              void* q_rot, uint8_t* k_pool, uint8_t* v_pool, uint8_t* k_scale,
+                              uint8_t* v_scale, const int32_t* frozen_len, uint32_t* status,
+                              cudaStream_t s);
+cudaError_t launch_attend_kv8(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_pool,
+                              const uint8_t* v_pool, const uint8_t* k_scale,
+                              const uint8_t* v_scale, const uint32_t* mask_words,
+                              uint32_t* status, cudaStream_t s);
 cudaError_t launch_combine(const pie_fwd_plan_t& p, void* out_readout, float* lse_readout,
                            void* out_all, float* lse_all, cudaStream_t s);
 

@@ -19,6 +19,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -93,6 +94,12 @@ struct HostPlan {
   std::vector<MaskBlock> mblocks;
   int64_t list_total = 0, cmask_total = 0;
   int mblock_max_nw = 0, mblock_max_rows = 0;
+  bool kv8 = false;
+  int window = 0, sinks = 0, sink_pages = 0;
+  std::vector<uint64_t> rope_turn;
+  std::vector<WriteBlock> wblocks;
+  std::vector<int32_t> wrow;
+  std::vector<DecItem> wide;
   bool has_mask = false, any_channel = false;
   bool dec_lists = false;  // some split-KV item walks a compacted list
   std::vector<int32_t> row_lane, readout;
@@ -154,8 +161,59 @@ int device_sm_count() {
   return v;
 }
 
-static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, HostPlan& H) {
+// The pages that a pass writes in a cache of 8-bit codes: every page's rows
+// share one scale per kv head, so one page is one unit of the append kernel
+// and at most one lane's page-table entry may write it.
+static int build_write_blocks(const pie_fwd_desc& D, const pie_fwd_meta& M, HostPlan& H) {
+  const int P = D.page_size;
+  H.wrow.resize(H.N);
+  for (int l = 0; l < H.L; ++l) {
+    const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1];
+    bool sorted = true;
+    for (int r = r0; r < r1; ++r) {
+      H.wrow[r] = r;
+      sorted = sorted && (r == r0 || M.slots[r] > M.slots[r - 1]);
+    }
+    if (!sorted)
+      std::sort(H.wrow.begin() + r0, H.wrow.begin() + r1,
+                [&](int32_t a, int32_t b) { return M.slots[a] < M.slots[b]; });
+    for (int i = r0; i < r1;) {
+      const int lp = M.slots[H.wrow[i]] / P;
+      WriteBlock b{l, lp, M.page_ids[M.page_indptr[l] + lp], i, 0, 0u, 0, 0};
+      for (; i < r1 && M.slots[H.wrow[i]] / P == lp; ++i) {
+        ++b.nrows;
+        b.written |= 1u << (M.slots[H.wrow[i]] % P);
+      }
+      H.wblocks.push_back(b);
+    }
+  }
+  static thread_local std::vector<int32_t> pages;
+  pages.clear();
+  for (const WriteBlock& b : H.wblocks) pages.push_back(b.page);
+  std::sort(pages.begin(), pages.end());
+  if (std::adjacent_find(pages.begin(), pages.end()) != pages.end())
+    return fail(PIE_EINVAL, "two lanes write one page of an 8-bit cache (its slots share a scale)");
+  return PIE_OK;
+}
+
+static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
+                           const pie_fwd_meta* meta, HostPlan& H) {
   if (!desc || !meta) return fail(PIE_EINVAL, "desc and meta are required");
+  H.kv8 = false;
+  H.window = H.sinks = H.sink_pages = 0;
+  if (cache) {
+    if (cache->kv_type != PIE_KV_DTYPE && cache->kv_type != PIE_KV_E4M3)
+      return fail(PIE_EINVAL, "unknown kv_type");
+    if (cache->window < 0 || cache->sinks < 0)
+      return fail(PIE_ERANGE, "window and sinks must not be negative");
+    if (cache->sinks > 0 && cache->window == 0)
+      return fail(PIE_EINVAL, "sinks without a window");
+    if (cache->window > 0 && meta->mask_word_indptr)
+      return fail(PIE_EINVAL, "a pass has a window or a mask, not both");
+    H.kv8 = cache->kv_type == PIE_KV_E4M3;
+    H.window = cache->window;
+    H.sinks = cache->sinks;
+  }
   const pie_fwd_desc& D = *desc;
   const pie_fwd_meta& M = *meta;
   if (D.num_q_heads <= 0 || D.num_kv_heads <= 0 || D.head_dim <= 0 || D.page_size <= 0)
@@ -167,6 +225,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
     return fail(PIE_EUNSUPPORTED, "head_dim must be 64 or 128 and page_size 8, 16 or 32");
   const int G = D.num_q_heads / D.num_kv_heads;
   if (G > 8) return fail(PIE_EUNSUPPORTED, "more than 8 q heads per kv head is not built");
+  H.sink_pages = static_cast<int>((static_cast<int64_t>(H.sinks) + D.page_size - 1) / D.page_size);
   if (!(D.rope_base > 0.0f)) return fail(PIE_EINVAL, "rope_base must be positive");
 
   const int L = M.num_lanes, N = M.num_rows;
@@ -278,6 +337,21 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
   for (int i = 0; i < d / 2; ++i)
     H.rope_freq[i] = static_cast<float>(std::pow(static_cast<double>(D.rope_base), -2.0 * i / d));
 
+  H.wblocks.clear();
+  H.wrow.clear();
+  H.rope_turn.clear();
+  if (H.kv8) {
+    // turns per position, base^(-2i/d) / (2 pi), whole turns dropped
+    H.rope_turn.resize(d / 2);
+    for (int i = 0; i < d / 2; ++i) {
+      const double t = std::pow(static_cast<double>(D.rope_base), -2.0 * i / d) /
+                       6.283185307179586476925;
+      H.rope_turn[i] = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 64));
+    }
+    const int rc = build_write_blocks(D, M, H);
+    if (rc != PIE_OK) return rc;
+  }
+
   // ---- work lists ---------------------------------------------------------
   const int Hkv = D.num_kv_heads;
   // query vectors per split-KV item: a whole GQA group of as many rows as
@@ -292,6 +366,22 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
     int mx = -1;
     for (int r = r0; r < r1; ++r) mx = std::max(mx, M.slots[r]);
     return std::min(kv, mx + 1);
+  };
+  // the slots a block of rows reads: their number and, in a windowed pass, the
+  // pages left out between the sink pages and the page of the first row's
+  // window (rows see nothing of them)
+  auto reads = [&](int l, int r0, int r1, int* skip) {
+    *skip = 0;
+    const int end = extent(l, r0, r1);
+    if (H.window == 0) return end;
+    int64_t first = INT32_MAX;
+    for (int r = r0; r < r1; ++r) first = std::min<int64_t>(first, M.slots[r]);
+    first = std::max<int64_t>(0, first - H.window + 1) / D.page_size;  // page of the window
+    const int64_t sink_slots = static_cast<int64_t>(H.sink_pages) * D.page_size;
+    if (first <= H.sink_pages) return end;
+    if (end <= first * D.page_size) return static_cast<int>(std::min<int64_t>(end, sink_slots));
+    *skip = static_cast<int>(first) - H.sink_pages;
+    return end - *skip * D.page_size;
   };
   // (the tensor-core kernel addresses pool rows with 32-bit TMA coordinates)
   const bool tc_ok = D.dtype == PIE_BF16 && D.head_dim == 128 &&
@@ -310,13 +400,30 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
   // split-KV kernel.
   auto lane_tc = [&](int l) {
     const int n = M.row_indptr[l + 1] - M.row_indptr[l];
+    if (H.kv8) return false;
     return tc_ok && n > 0 && (n * G >= kTcMinQueries || (H.has_mask && !mma_ok));
   };
-  auto lane_list = [&](int l) { return H.has_mask && (lane_tc(l) || mma_ok); };
+  auto lane_list = [&](int l) { return !H.kv8 && H.has_mask && (lane_tc(l) || mma_ok); };
+  // 8-bit caches: lanes with more query vectors per kv head than one item's 8
+  // take wide items, which convert each code once for up to 32 of them
+  auto lane_wide = [&](int l) {
+    return H.kv8 && (M.row_indptr[l + 1] - M.row_indptr[l]) * G > 8;
+  };
+  const int wide_rows = std::max(1, kWideQueries / G);
   // split-KV items: chunk length from the total work
   int64_t work = 0;
-  for (int l = 0; l < L; ++l)
-    if (!lane_tc(l)) work += static_cast<int64_t>(M.kv_len[l]) * Hkv;
+  for (int l = 0; l < L; ++l) {
+    if (lane_tc(l)) continue;
+    int64_t slots = M.kv_len[l];
+    const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1];
+    if (H.window > 0 || H.kv8) {
+      slots = 0;
+      const int rows = lane_wide(l) ? wide_rows : rows_per_item;
+      int skip;
+      for (int b0 = r0; b0 < r1; b0 += rows) slots += reads(l, b0, std::min(r1, b0 + rows), &skip);
+    }
+    work += slots * Hkv;
+  }
   const int CH = choose_chunk(work);
   // tensor-core items: two query tiles per item when some lane has more than
   // 128 query vectors per kv head (they then share every K/V tile)
@@ -333,7 +440,8 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
     if (!lane_tc(l)) continue;
     const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1];
     for (int b0 = r0; b0 < r1; b0 += tc_rows) {
-      tc_total += static_cast<int64_t>(extent(l, b0, std::min(r1, b0 + tc_rows))) * Hkv;
+      int skip;
+      tc_total += static_cast<int64_t>(reads(l, b0, std::min(r1, b0 + tc_rows), &skip)) * Hkv;
       tc_units += Hkv;
     }
   }
@@ -344,6 +452,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
   H.num_comb_merge = 0;
   H.row_block.assign(N, 0);
   H.dec.clear();
+  H.wide.clear();
   H.tc.clear();
   // masked passes: the list-walking lanes' items walk the compacted list of
   // the slots their row block can see (one list per row block, shared by all
@@ -381,13 +490,15 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
     const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1], n = r1 - r0;
     if (n == 0) continue;
     const bool use_tc = lane_tc(l);
-    const int blk_rows = use_tc ? tc_rows : rows_per_item;
-    const int stride = use_tc ? kTcTileQueries : H.nq;
+    const bool wide = lane_wide(l);
+    const int blk_rows = use_tc ? tc_rows : wide ? wide_rows : rows_per_item;
+    const int stride = use_tc ? kTcTileQueries : wide ? kWideQueries : H.nq;
     for (int b0 = r0; b0 < r1; b0 += blk_rows) {
       const int b1 = std::min(r1, b0 + blk_rows);
       const int32_t blk_id = static_cast<int32_t>(H.comb.size() / Hkv);
       for (int r = b0; r < b1; ++r) H.row_block[r] = blk_id;
-      const int ext = extent(l, b0, b1);
+      int skip;
+      const int ext = reads(l, b0, b1, &skip);
       int nchunks, chunk;
       if (use_tc) {
         nchunks = static_cast<int>(std::max<int64_t>(1, (ext + tc_ch / 2) / tc_ch));
@@ -412,20 +523,21 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
           for (int c = 0; c < nchunks; ++c) {
             const int kb = c * chunk, ke = std::min(ext, kb + chunk);
             H.tc.push_back(TcItem{l, g, b0, b1 - b0, kb, ke, static_cast<int32_t>(part),
-                                  direct ? 1 : 0, mblk, c, nchunks, 0});
+                                  direct ? 1 : 0, mblk, c, nchunks, skip});
             part += direct ? 0 : stride * H.tc_nt;
           }
         } else {
           // the unit's chunks written in place (a decode batch has thousands);
           // a listed item names its list block and its chunk of the list
-          const size_t base = H.dec.size();
-          H.dec.resize(base + nchunks);
-          DecItem* di = H.dec.data() + base;
+          std::vector<DecItem>& items = wide ? H.wide : H.dec;
+          const size_t base = items.size();
+          items.resize(base + nchunks);
+          DecItem* di = items.data() + base;
           for (int c = 0; c < nchunks; ++c) {
             const int kb = c * chunk;
             const int32_t pb = static_cast<int32_t>(part + int64_t(c) * stride);
             di[c] = mblk >= 0 ? DecItem{l, g, b0, b1 - b0, c, nchunks, pb, mblk}
-                              : DecItem{l, g, b0, b1 - b0, kb, std::min(ext, kb + chunk), pb, -1};
+                              : DecItem{l, g, b0, b1 - b0, kb, std::min(ext, kb + chunk), pb, -1 - skip};
           }
           part += int64_t(nchunks) * stride;
         }
@@ -460,7 +572,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, H
 struct Layout {
   size_t row_indptr, positions, slots, kv_len, page_indptr, page_ids, fold_mode, fold_count,
       row_lane, mask_word_indptr, readout, ro_indptr, ro_idx, rope_freq, dec, tc, comb, mblocks,
-      row_block;
+      row_block, rope_turn, wblocks, wrow, wide;
   size_t copy_bytes;  // everything above
   size_t part_o, part_ml, list, lrow, cmask, list_len, list_mode, mask_tiles, dec_work;
   size_t total;
@@ -495,9 +607,13 @@ static Layout make_layout(const pie_fwd_desc& D, const HostPlan& H) {
   Y.comb = take(sizeof(CombEntry) * H.comb.size());
   Y.row_block = take(sizeof(int32_t) * H.row_block.size());
   Y.mblocks = take(sizeof(MaskBlock) * H.mblocks.size());
+  Y.rope_turn = take(sizeof(uint64_t) * H.rope_turn.size());
+  Y.wblocks = take(sizeof(WriteBlock) * H.wblocks.size());
+  Y.wrow = take(sizeof(int32_t) * H.wrow.size());
+  Y.wide = take(sizeof(DecItem) * H.wide.size());
   // the split-KV kernel's work counter and finished-CTA count (zero from the
   // upload; the kernel sets them back to zero when it ends)
-  Y.dec_work = take(H.dec.empty() ? 0 : 2 * sizeof(int32_t));
+  Y.dec_work = take(H.kv8 ? 4 * sizeof(int32_t) : H.dec.empty() ? 0 : 2 * sizeof(int32_t));
   Y.copy_bytes = o;
   Y.part_o = take(sizeof(float) * static_cast<size_t>(H.num_part_slots) * D.head_dim);
   Y.part_ml = take(sizeof(float2) * static_cast<size_t>(H.num_part_slots));
@@ -564,9 +680,14 @@ static HostPlan& thread_host_plan() {
 }
 
 int pie_fwd_workspace_bytes(const pie_fwd_desc* desc, const pie_fwd_meta* meta, size_t* bytes) {
+  return pie_fwd_cache_workspace_bytes(desc, nullptr, meta, bytes);
+}
+
+int pie_fwd_cache_workspace_bytes(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
+                                  const pie_fwd_meta* meta, size_t* bytes) {
   if (!bytes) return fail(PIE_EINVAL, "bytes is NULL");
   HostPlan& H = thread_host_plan();
-  int rc = build_host_plan(desc, meta, H);
+  int rc = build_host_plan(desc, cache, meta, H);
   if (rc != PIE_OK) return rc;
   *bytes = make_layout(*desc, H).total;
   return PIE_OK;
@@ -574,10 +695,16 @@ int pie_fwd_workspace_bytes(const pie_fwd_desc* desc, const pie_fwd_meta* meta, 
 
 int pie_fwd_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, void* dev_workspace,
                  size_t ws_bytes, void* stream, pie_fwd_plan_t** out) {
+  return pie_fwd_cache_plan(desc, nullptr, meta, dev_workspace, ws_bytes, stream, out);
+}
+
+int pie_fwd_cache_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
+                       const pie_fwd_meta* meta, void* dev_workspace, size_t ws_bytes,
+                       void* stream, pie_fwd_plan_t** out) {
   if (!out) return fail(PIE_EINVAL, "out is NULL");
   *out = nullptr;
   HostPlan& H = thread_host_plan();
-  int rc = build_host_plan(desc, meta, H);
+  int rc = build_host_plan(desc, cache, meta, H);
   if (rc != PIE_OK) return rc;
   const pie_fwd_meta& M = *meta;
   Layout Y = make_layout(*desc, H);
@@ -613,6 +740,10 @@ int pie_fwd_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, void* dev_w
   put(Y.comb, H.comb.data(), sizeof(CombEntry) * H.comb.size());
   put(Y.row_block, H.row_block.data(), sizeof(int32_t) * H.row_block.size());
   put(Y.mblocks, H.mblocks.data(), sizeof(MaskBlock) * H.mblocks.size());
+  put(Y.rope_turn, H.rope_turn.data(), sizeof(uint64_t) * H.rope_turn.size());
+  put(Y.wblocks, H.wblocks.data(), sizeof(WriteBlock) * H.wblocks.size());
+  put(Y.wrow, H.wrow.data(), sizeof(int32_t) * H.wrow.size());
+  put(Y.wide, H.wide.data(), sizeof(DecItem) * H.wide.size());
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Y.copy_bytes > 0 &&
@@ -647,6 +778,9 @@ int pie_fwd_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, void* dev_w
   p->mblock_max_rows = H.mblock_max_rows;
   p->num_part_slots = H.num_part_slots;
   p->num_comb_merge = H.num_comb_merge;
+  p->kv8 = H.kv8;
+  p->num_wblocks = static_cast<int32_t>(H.wblocks.size());
+  p->num_wide_items = static_cast<int32_t>(H.wide.size());
   char* w = static_cast<char*>(dev_workspace);
   DevMeta& dm = p->dev;
   dm.row_indptr = reinterpret_cast<const int32_t*>(w + Y.row_indptr);
@@ -678,8 +812,16 @@ int pie_fwd_plan(const pie_fwd_desc* desc, const pie_fwd_meta* meta, void* dev_w
   dm.mask_tiles = reinterpret_cast<int32_t*>(w + Y.mask_tiles);
   // plain passes: a persistent grid takes the split-KV items from the counter;
   // list passes: fixed runs of kDecListItemsPerCta items per CTA
-  dm.dec_work = (H.dec.empty() || H.dec_lists) ? nullptr
-                                                : reinterpret_cast<int32_t*>(w + Y.dec_work);
+  dm.dec_work = ((H.dec.empty() && !H.kv8) || H.dec_lists)
+                    ? nullptr
+                    : reinterpret_cast<int32_t*>(w + Y.dec_work);
+  dm.rope_turn = reinterpret_cast<const uint64_t*>(w + Y.rope_turn);
+  dm.wblocks = reinterpret_cast<const WriteBlock*>(w + Y.wblocks);
+  dm.wrow = reinterpret_cast<const int32_t*>(w + Y.wrow);
+  dm.wide_items = reinterpret_cast<const DecItem*>(w + Y.wide);
+  dm.window = H.window;
+  dm.sinks = H.sinks;
+  dm.sink_pages = H.sink_pages;
   dm.num_sms = H.sms;
   dm.num_pool_pages = M.num_pool_pages;
   p->staging = blk;
@@ -699,6 +841,7 @@ int pie_fwd_append_kv(const pie_fwd_plan_t* plan, const void* q, const void* k, 
                       void* q_rot, void* k_pool, void* v_pool, const int32_t* frozen_len,
                       uint32_t* status, void* stream) {
   if (!plan) return fail(PIE_EINVAL, "plan is NULL");
+  if (plan->kv8) return fail(PIE_EINVAL, "append_kv: the plan's cache holds 8-bit codes");
   if (plan->N == 0) return PIE_OK;
   if (!q || !k || !v || !q_rot || !k_pool || !v_pool || !frozen_len)
     return fail(PIE_EINVAL, "append_kv: a required pointer is NULL");
@@ -713,6 +856,7 @@ int pie_fwd_attend(const pie_fwd_plan_t* plan, const void* q_rot, const void* k_
                    float* lse_readout, void* out_all, float* lse_all, uint32_t* status,
                    void* stream) {
   if (!plan) return fail(PIE_EINVAL, "plan is NULL");
+  if (plan->kv8) return fail(PIE_EINVAL, "attend: the plan's cache holds 8-bit codes");
   if (plan->has_mask && !mask_words) return fail(PIE_EINVAL, "the plan has a mask: mask_words required");
   if (!plan->has_mask && mask_words) return fail(PIE_EINVAL, "mask_words given but the plan has no mask");
   if (plan->N == 0) return PIE_OK;
@@ -738,6 +882,86 @@ int pie_fwd_attend(const pie_fwd_plan_t* plan, const void* q_rot, const void* k_
   return PIE_OK;
 }
 
+// some required row, pool or output address is off the 16-byte vectors' boundary
+static bool misaligned(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return true;
+  return false;
+}
+
+int pie_fwd_append_kv8(const pie_fwd_plan_t* plan, const void* q, const void* k, const void* v,
+                       void* q_rot, uint8_t* k_pool, uint8_t* v_pool, uint8_t* k_scale,
+                       uint8_t* v_scale, const int32_t* frozen_len, uint32_t* status,
+                       void* stream) {
+  if (!plan) return fail(PIE_EINVAL, "plan is NULL");
+  if (!plan->kv8) return fail(PIE_EINVAL, "append_kv8: the plan's cache does not hold 8-bit codes");
+  if (plan->N == 0) return PIE_OK;
+  if (!q || !k || !v || !q_rot || !k_pool || !v_pool || !k_scale || !v_scale || !frozen_len)
+    return fail(PIE_EINVAL, "append_kv8: a required pointer is NULL");
+  if (misaligned({q, k, v, q_rot, k_pool, v_pool}))
+    return fail(PIE_EINVAL, "append_kv8: rows and pools must be 16-byte aligned");
+  cudaError_t e = launch_append_kv8(*plan, q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale,
+                                    frozen_len, status, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(PIE_ECUDA, std::string("append_kv8 launch: ") + cudaGetErrorString(e));
+  return PIE_OK;
+}
+
+int pie_fwd_attend_kv8(const pie_fwd_plan_t* plan, const void* q_rot, const uint8_t* k_pool,
+                       const uint8_t* v_pool, const uint8_t* k_scale, const uint8_t* v_scale,
+                       const uint32_t* mask_words, void* out_readout, float* lse_readout,
+                       void* out_all, float* lse_all, uint32_t* status, void* stream) {
+  if (!plan) return fail(PIE_EINVAL, "plan is NULL");
+  if (!plan->kv8) return fail(PIE_EINVAL, "attend_kv8: the plan's cache does not hold 8-bit codes");
+  if (plan->has_mask && !mask_words) return fail(PIE_EINVAL, "the plan has a mask: mask_words required");
+  if (!plan->has_mask && mask_words) return fail(PIE_EINVAL, "mask_words given but the plan has no mask");
+  if (plan->N == 0) return PIE_OK;
+  if (!q_rot || !k_pool || !v_pool || !k_scale || !v_scale)
+    return fail(PIE_EINVAL, "attend_kv8: q_rot, pools and scales are required");
+  if (plan->R > 0 && !out_readout && !out_all)
+    return fail(PIE_EINVAL, "attend_kv8: out_readout (or out_all) is required");
+  if (misaligned({q_rot, k_pool, v_pool, out_readout, out_all}))
+    return fail(PIE_EINVAL, "attend_kv8: rows and pools must be 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (g_ev_start) e = cudaEventRecord(g_ev_start, s);
+  if (e == cudaSuccess)
+    e = launch_attend_kv8(*plan, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words, status, s);
+  if (e == cudaSuccess && g_ev_stop) e = cudaEventRecord(g_ev_stop, s);
+  if (e == cudaSuccess && plan->num_comb_merge > 0)
+    e = launch_combine(*plan, out_readout, lse_readout, out_all, lse_all, s);
+  if (e != cudaSuccess) return fail(PIE_ECUDA, std::string("attend_kv8 launch: ") + cudaGetErrorString(e));
+  return PIE_OK;
+}
+
+int pie_fwd_forward_cache(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
+                          const pie_fwd_meta* meta, void* dev_workspace, size_t ws_bytes,
+                          const void* q, const void* k, const void* v, void* q_rot, void* k_pool,
+                          void* v_pool, uint8_t* k_scale, uint8_t* v_scale, int32_t* frozen_len,
+                          const uint32_t* mask_words, void* out_readout, float* lse_readout,
+                          void* out_all, float* lse_all, const int32_t* channel,
+                          uint32_t* status, void* stream) {
+  pie_fwd_plan_t* plan = nullptr;
+  int rc = pie_fwd_cache_plan(desc, cache, meta, dev_workspace, ws_bytes, stream, &plan);
+  if (rc != PIE_OK) return rc;
+  uint8_t *k8 = static_cast<uint8_t*>(k_pool), *v8 = static_cast<uint8_t*>(v_pool);
+  if (plan->kv8) {
+    rc = pie_fwd_append_kv8(plan, q, k, v, q_rot, k8, v8, k_scale, v_scale, frozen_len, status,
+                            stream);
+    if (rc == PIE_OK)
+      rc = pie_fwd_attend_kv8(plan, q_rot, k8, v8, k_scale, v_scale, mask_words, out_readout,
+                              lse_readout, out_all, lse_all, status, stream);
+  } else {
+    rc = pie_fwd_append_kv(plan, q, k, v, q_rot, k_pool, v_pool, frozen_len, status, stream);
+    if (rc == PIE_OK && plan->has_mask && mask_words) rc = pie_fwd_set_mask(plan, mask_words, stream);
+    if (rc == PIE_OK)
+      rc = pie_fwd_attend(plan, q_rot, k_pool, v_pool, mask_words, out_readout, lse_readout,
+                          out_all, lse_all, status, stream);
+  }
+  if (rc == PIE_OK) rc = pie_fwd_fold(plan, frozen_len, channel, status, stream);
+  pie_fwd_plan_destroy(plan);
+  return rc;
+}
+
 int pie_fwd_set_mask(pie_fwd_plan_t* plan, const uint32_t* mask_words, void* stream) {
   if (!plan) return fail(PIE_EINVAL, "plan is NULL");
   if (!plan->has_mask) return fail(PIE_EINVAL, "set_mask: the plan has no mask");
@@ -757,17 +981,9 @@ int pie_fwd_forward(const pie_fwd_desc* desc, const pie_fwd_meta* meta, void* de
                     void* k_pool, void* v_pool, int32_t* frozen_len, const uint32_t* mask_words,
                     void* out_readout, float* lse_readout, void* out_all, float* lse_all,
                     const int32_t* channel, uint32_t* status, void* stream) {
-  pie_fwd_plan_t* plan = nullptr;
-  int rc = pie_fwd_plan(desc, meta, dev_workspace, ws_bytes, stream, &plan);
-  if (rc != PIE_OK) return rc;
-  rc = pie_fwd_append_kv(plan, q, k, v, q_rot, k_pool, v_pool, frozen_len, status, stream);
-  if (rc == PIE_OK && plan->has_mask && mask_words) rc = pie_fwd_set_mask(plan, mask_words, stream);
-  if (rc == PIE_OK)
-    rc = pie_fwd_attend(plan, q_rot, k_pool, v_pool, mask_words, out_readout, lse_readout,
-                        out_all, lse_all, status, stream);
-  if (rc == PIE_OK) rc = pie_fwd_fold(plan, frozen_len, channel, status, stream);
-  pie_fwd_plan_destroy(plan);
-  return rc;
+  return pie_fwd_forward_cache(desc, nullptr, meta, dev_workspace, ws_bytes, q, k, v, q_rot, k_pool,
+                               v_pool, nullptr, nullptr, frozen_len, mask_words, out_readout,
+                               lse_readout, out_all, lse_all, channel, status, stream);
 }
 
 int pie_fwd_fold(const pie_fwd_plan_t* plan, int32_t* frozen_len, const int32_t* channel,
