@@ -33,8 +33,8 @@
 // warp) streams an item's chunk through a ring of tensor copies with a swizzle
 // that keeps ldmatrix free of bank conflicts; a persistent grid takes items from
 // a counter.  Items hold up to 8 query vectors (NT = 1: decode rows, bound by
-// HBM: a slot and kv head costs 2 d bytes) or 32 (NT = 4: drafts and prompts,
-// every code converted once for all of them).
+// HBM: a slot and kv head costs 2 d bytes) or 32 (NT = 4: drafts and prompts
+// that attend_kv8_tc.cu does not take, every code converted once for all of them).
 // Masked passes skip stages that no row of the item sees.  Every wait is
 // bounded in time.
 
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
         for (int e = 0; e < EPT; ++e) big = fmaxf(big, fabsf(x[e]));
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-        const int up = 13 - (int(__float_as_uint(big) >> 23) - 127);
+        const int up = fp8::query_exp(big);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) x[e] = fp8::scale2(x[e], up);
         uint32_t* dst = reinterpret_cast<uint32_t*>(qs + qv * C::QROW + ch * EPT * 2);
@@ -641,7 +641,6 @@ cudaError_t launch_attend_kv8(const pie_fwd_plan_t& p, const void* q_rot, const 
                               const uint8_t* v_pool, const uint8_t* k_scale,
                               const uint8_t* v_scale, const uint32_t* mask_words,
                               uint32_t* status, cudaStream_t s) {
-  if (p.num_dec_items + p.num_wide_items == 0) return cudaSuccess;
   const int D = p.desc.head_dim, P = p.desc.page_size;
   CUtensorMap km, vm;
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(P),

@@ -1,0 +1,603 @@
+// Step 2-3 of a ForwardPass over a cache of 8-bit codes for lanes with many
+// query vectors per kv head (drafts, prompts), bf16 passes with head_dim 128:
+// grouped-query attention on the 5th-generation tensor cores (Pie "The forward
+// pass", State geometry: kv_len; Attention masks; Readouts).
+//
+// The mathematics is that of attend_kv8.cu: fp16 operands (codes exact, query
+// vectors scaled by a power of two each, weights to 11 bits), K's scale on the
+// scores, V's in the exponent, a whole-number running maximum.
+//
+// One CTA takes a work item: NT (1 or 2) tiles of 128 query vectors against a
+// chunk of the lane's slots, in tiles of BN = 64 slots.
+//   warp 0       producer: the codes of a tile's pages, one tensor copy per page
+//                and tensor, into a ring of raw stages;
+//   warps 1..NT  one MMA issuer per query tile: S = Q K^T (128 x 64) into one of
+//                two TMEM score buffers, O += P V (128 x 128) with P in TMEM;
+//   2 or 4 warps converters: raw codes (16 per thread and step) to fp16 in the
+//                128-byte-swizzled operand layout, rows past the end as zeros;
+//                one conversion serves all query tiles;
+//   4 NT warps   softmax: a thread per query row (its TMEM lane), which first
+//                writes its own scaled query vector into the operand tile.
+// Scores of tile j + 2 are issued behind P.V of tile j, so a softmax step never
+// waits for them.  The conversion costs 1 shared load, 8 conversions and 2
+// shared stores per 16 codes, about a third of the softmax's issue slots with
+// NT = 2, and runs beside it.  Masked passes walk only the tiles some row of the
+// item sees, listed once at the start.  Every wait is bounded in time.
+
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "tc_util.cuh"
+#include "tmem128.cuh"
+
+namespace pie {
+
+namespace t8 {
+
+constexpr int D = 128;
+constexpr int BN = 64;                    // slots per tile
+constexpr int RAW = 2 * BN * D;           // raw codes of a tile, K then V: 16 KB
+constexpr int HALF = BN * 128;            // fp16 operand, half of d: 8 KB
+constexpr int MAX_PAGES = BN / 8;
+constexpr int MAX_TILES = 2048;           // of a masked item (the planner's chunks are shorter)
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+template <int NT>
+struct Cfg {
+  static constexpr int RS = NT == 1 ? 5 : 3;  // raw stages
+  static constexpr int NS = 3;                // operand stages
+  static constexpr int CONVERTERS = NT == 1 ? 4 : 2;  // warps (two leave the softmax its registers)
+  static constexpr int kIssuer0 = 1;
+  static constexpr int kConv0 = 1 + NT;
+  static constexpr int kSoft0 = kConv0 + CONVERTERS;
+  static constexpr int kThreads = 32 * kSoft0 + 128 * NT;
+  static constexpr uint32_t kTmemCols = NT == 1 ? 256 : 512;
+};
+
+template <int NT>
+struct __align__(1024) Smem {
+  using C = Cfg<NT>;
+  uint8_t q[NT][2][128 * 128];     // [query tile][half of d][row][128 B]
+  uint8_t raw[C::RS][RAW];
+  uint8_t k[C::NS][2][HALF];       // [half of d][slot][128 B]
+  uint8_t v[C::NS][2][HALF];
+  int exps[C::RS][2][MAX_PAGES];   // exponents of the raw tile's pages, K and V
+  float4 sc[C::NS][BN / 8];        // per 8 slots: 2^ek, ev, 2^-ev
+  uint16_t tiles[MAX_TILES];       // masked items: the tiles that are seen
+  uint64_t q_full;
+  uint64_t raw_full[C::RS], raw_empty[C::RS];
+  uint64_t k_full[C::NS], v_full[C::NS], kv_empty[C::NS];
+  uint64_t s_full[NT][2], p_full[NT][2], o_done[NT][2];
+  uint64_t mma_done[NT];
+  uint32_t tmem_base;
+  int num_tiles, warp_tiles[16];
+};
+
+// kind::f16 with fp16 A and B, fp32 accumulator, A K-major, B K-major or MN-major
+constexpr uint32_t idesc16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// score buffer b of query tile t at columns (2t + b) 64, O at 2 NT 64 + 128 t
+template <int NT>
+__device__ __forceinline__ uint32_t s_col(int t, int b) { return uint32_t(BN) * (2 * t + b); }
+template <int NT>
+__device__ __forceinline__ uint32_t o_col(int t) { return uint32_t(2 * NT * BN + 128 * t); }
+
+__device__ __forceinline__ void ld64(uint32_t taddr, float* f) {
+  uint32_t r[64];
+  asm volatile(PIE_TMEM_LD64_ASM : PIE_TMEM_LD64_OUTS : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void st64(uint32_t taddr, const float* f) {
+  uint32_t r[64];
+#pragma unroll
+  for (int i = 0; i < 64; ++i) r[i] = __float_as_uint(f[i]);
+  asm volatile(PIE_TMEM_ST64_ASM ::"r"(taddr), PIE_TMEM_ST64_INS : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(PIE_TMEM_ST32_ASM ::"r"(taddr), PIE_TMEM_ST32_INS : "memory");
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int z, uint64_t* bar,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(0), "r"(0), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+}  // namespace t8
+
+template <int NT>
+__global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel(
+    DevMeta m, int G, int Hq, int Hkv, int P, float scale_log2, const __nv_bfloat16* q_rot,
+    const uint8_t* k_scale, const uint8_t* v_scale, const uint32_t* mask_words, tc::Out out,
+    uint32_t* status, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap vmap) {
+  using namespace t8;
+  using C = Cfg<NT>;
+  constexpr int RS = C::RS, NS = C::NS;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<NT>& S = *reinterpret_cast<Smem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const TcItem it = m.tc_items[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kb = it.kv_begin, ke = it.kv_end;
+  const int nqv = it.nrows * G;
+  const int all_tiles = ke > kb ? (ke - kb + BN - 1) / BN : 0;
+  const WindowView view(m, P, it.skip);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&S.q_full, 4 * NT);
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(&S.raw_full[i], 1);
+      mbar_init(&S.raw_empty[i], C::CONVERTERS);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&S.k_full[i], C::CONVERTERS);
+      mbar_init(&S.v_full[i], C::CONVERTERS);
+      mbar_init(&S.kv_empty[i], NT);
+    }
+    for (int t = 0; t < NT; ++t) {
+      mbar_init(&S.mma_done[t], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&S.s_full[t][b], 1);
+        mbar_init(&S.p_full[t][b], 4);
+        mbar_init(&S.o_done[t][b], 1);
+      }
+    }
+    fence_barrier_init();
+  }
+  if (warp == C::kIssuer0 && all_tiles > 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&S.tmem_base)),
+                 "r"(C::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // everything above is the plan's; the masks, queries and codes are read below
+  grid_dep_wait();
+  grid_dep_launch();
+  int T = all_tiles;
+  if (mask_words) {
+    // the tiles some row of the item sees, in order (a thread per tile)
+    T = 0;
+    for (int base = 0; base < all_tiles; base += C::kThreads) {
+      const int j = base + int(threadIdx.x), sb = kb + j * BN;
+      bool seen = false;
+      if (j < all_tiles)
+        for (int r = 0; r < it.nrows && !seen; ++r) {
+          const uint32_t* w = mask_words + m.mask_word_indptr[it.row0 + r] + (sb >> 5);
+#pragma unroll
+          for (int i = 0; i < BN / 32; ++i) {
+            const int left = ke - sb - 32 * i;
+            if (left > 0) seen = seen || (w[i] & (left < 32 ? (1u << left) - 1u : ~0u)) != 0;
+          }
+        }
+      const uint32_t bits = __ballot_sync(0xffffffffu, seen);
+      if (lane == 0) S.warp_tiles[warp] = __popc(bits);
+      __syncthreads();
+      int at = T;
+      for (int w = 0; w < C::kThreads / 32; ++w) {
+        if (w < warp) at += S.warp_tiles[w];
+        T += S.warp_tiles[w];
+      }
+      if (seen) S.tiles[at + __popc(bits & ((1u << lane) - 1u))] = uint16_t(j);
+      __syncthreads();
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = S.tmem_base;
+  bool bad = false;
+  // first slot position of the item's j-th tile
+  auto tile_at = [&](int j) { return kb + (mask_words ? int(S.tiles[j]) : j) * BN; };
+
+  if (warp == 0) {
+    // ---------------- producer -----------------------------------------------
+    // lane 2i + c: the K (c = 0) or V (1) codes of the tile's page i, and the
+    // exponent of its scale; page ids two tiles ahead, exponents one
+    const uint64_t pol = policy_evict_first();
+    const int c = lane & 1, pi = lane >> 1;
+    const uint8_t* scale = c ? v_scale : k_scale;
+    const int32_t* pages = m.page_ids + m.page_indptr[it.lane];
+    auto page_of = [&](int j) -> int {
+      if (j >= T || pi >= MAX_PAGES) return -1;
+      const int ts = tile_at(j), pg = ts / P + pi;
+      if (pg > (min(ts + BN, ke) - 1) / P) return -1;
+      return pages[pg + (pg >= m.sink_pages ? it.skip : 0)];
+    };
+    auto exp_of = [&](int pid) -> int {
+      return pid >= 0 && pid < m.num_pool_pages
+                 ? int(scale[int64_t(pid) * Hkv + it.kv_head]) - fp8::kBias : 0;
+    };
+    int pid = page_of(0), pid1 = page_of(1);
+    int ex = exp_of(pid);
+    for (int j = 0; j < T; ++j) {
+      const int st = j % RS;
+      if (j >= RS && !mbar_wait(&S.raw_empty[st], ((j / RS) - 1) & 1)) {
+        bad = true;
+        break;
+      }
+      const bool issue = pid >= 0 && pid < m.num_pool_pages;
+      const uint32_t copies = __popc(__ballot_sync(0xffffffffu, issue));
+      if (pi < MAX_PAGES) S.exps[st][c][pi] = ex;
+      __syncwarp();
+      if (lane == 0) {
+        const int ts = tile_at(j);
+        if (copies != 2u * uint32_t((min(ts + BN, ke) - 1) / P - ts / P + 1))
+          set_status(status, PIE_STATUS_BOUNDS);
+        mbar_arrive_expect_tx(&S.raw_full[st], copies * uint32_t(P) * D);
+      }
+      __syncwarp();
+      if (issue)
+        tma_3d(S.raw[st] + c * BN * D + pi * P * D, c ? &vmap : &kmap,
+               int(int64_t(pid) * Hkv + it.kv_head), &S.raw_full[st], pol);
+      pid = pid1;
+      ex = exp_of(pid);
+      pid1 = page_of(j + 2);
+    }
+  } else if (warp < C::kConv0) {
+    // ---------------- MMA issuers ----------------------------------------------
+    if (lane == 0 && T > 0) {
+      const int t = warp - C::kIssuer0;
+      constexpr uint32_t ID_S = idesc16(128, BN, false);
+      constexpr uint32_t ID_O = idesc16(128, 128, true);
+      const uint64_t dq = tc::sdesc(S.q[t][0], 16, 1024);
+      const uint64_t dk = tc::sdesc(S.k[0][0], 16, 1024);
+      const uint64_t dv = tc::sdesc(S.v[0][0], HALF, 1024);
+      const uint32_t tO = tmem + o_col<NT>(t);
+      auto issue_s = [&](int j) -> bool {
+        const int st = j % NS;
+        if (!mbar_wait(&S.k_full[st], (j / NS) & 1)) return false;
+        tc::fence_after();
+        const uint64_t bk = dk + uint64_t(st) * (2 * HALF >> 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc::mma_ss(tmem + s_col<NT>(t, j & 1), dq + uint64_t((k >> 2) * (128 * 128 >> 4) + (k & 3) * 2),
+                     bk + uint64_t((k >> 2) * (HALF >> 4) + (k & 3) * 2), ID_S, k > 0 ? 1u : 0u);
+        tc::commit(&S.s_full[t][j & 1]);
+        return true;
+      };
+      auto issue_pv = [&](int j) -> bool {
+        if (!mbar_wait(&S.p_full[t][j & 1], (j >> 1) & 1)) return false;
+        const int st = j % NS;
+        if (!mbar_wait(&S.v_full[st], (j / NS) & 1)) return false;
+        tc::fence_after();
+        const int ksteps = (min(BN, ke - tile_at(j)) + 15) >> 4;
+        const uint64_t bv = dv + uint64_t(st) * (2 * HALF >> 4);
+        const uint32_t ta = tmem + s_col<NT>(t, j & 1);
+        for (int k = 0; k < ksteps; ++k)
+          tc::mma_ts(tO, ta + 8 * k, bv + uint64_t(k) * (2048 >> 4), ID_O, (j > 0 || k > 0) ? 1u : 0u);
+        tc::commit(&S.o_done[t][j & 1]);
+        tc::commit(&S.kv_empty[st]);
+        return true;
+      };
+      bool ok = mbar_wait(&S.q_full, 0);
+      tc::fence_after();
+      for (int j = 0; j < 2 && j < T && ok; ++j) ok = issue_s(j);
+      for (int j = 0; j < T && ok; ++j) {
+        ok = issue_pv(j);
+        if (ok && j + 2 < T) ok = issue_s(j + 2);
+      }
+      // every MMA of this issuer has finished before TMEM is released
+      tc::commit(&S.mma_done[t]);
+      if (!mbar_wait(&S.mma_done[t], 0)) ok = false;
+      bad = !ok;
+    }
+  } else if (warp < C::kSoft0) {
+    // ---------------- converters -------------------------------------------------
+    // thread: 16-byte chunk c of rows r0, r0 + RSTEP, ..; its 16 codes become two
+    // 16-byte chunks of the operand row (half c / 4 of d).  The upper half's
+    // threads write their two chunks in the other order, so that the 8
+    // threads of a row's store hit 8 distinct banks.
+    const int ct = threadIdx.x - 32 * C::kConv0;
+    constexpr int RSTEP = 4 * C::CONVERTERS;
+    const int c = ct & 7, r0 = ct >> 3, h = c >> 2;
+    for (int j = 0; j < T; ++j) {
+      const int rs = j % RS, st = j % NS;
+      if (!mbar_wait(&S.raw_full[rs], (j / RS) & 1) ||
+          (j >= NS && !mbar_wait(&S.kv_empty[st], ((j / NS) - 1) & 1))) {
+        bad = true;
+        break;
+      }
+      const int valid = min(BN, ke - tile_at(j));
+      if (ct < BN / 8) {
+        const int pg = 8 * ct / P;
+        const int ev = S.exps[rs][1][pg];
+        S.sc[st][ct] = make_float4(fp8::pow2i(S.exps[rs][0][pg]), float(ev), fp8::pow2i(-ev), 0.f);
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t* src = S.raw[rs] + kv * BN * D;
+        uint8_t* dst = kv ? S.v[st][h] : S.k[st][h];
+#pragma unroll
+        for (int i = 0; i < BN / RSTEP; ++i) {
+          const int r = r0 + RSTEP * i;
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (r < valid) u = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
+          uint32_t f[8];
+          fp8::to_half2x2(u.x, f[0], f[1]);
+          fp8::to_half2x2(u.y, f[2], f[3]);
+          fp8::to_half2x2(u.z, f[4], f[5]);
+          fp8::to_half2x2(u.w, f[6], f[7]);
+          const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), b = make_uint4(f[4], f[5], f[6], f[7]);
+          const int dc = 2 * (c & 3);
+          uint8_t* row = dst + r * 128;
+          *reinterpret_cast<uint4*>(row + (((dc + h) ^ (r & 7)) << 4)) = h ? b : a;
+          *reinterpret_cast<uint4*>(row + (((dc + 1 - h) ^ (r & 7)) << 4)) = h ? a : b;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kv ? &S.v_full[st] : &S.k_full[st]);
+          if (kv) mbar_arrive(&S.raw_empty[rs]);
+        }
+      }
+    }
+  } else if (T > 0) {
+    // ---------------- softmax groups: thread = query row ---------------------
+    const int t = (warp - C::kSoft0) >> 2;
+    const int quad = warp & 3;
+    const int qm = quad * 32 + lane;  // row of the query tile == TMEM lane
+    const int q = t * kTcTileQueries + qm;
+    const bool valid_q = q < nqv;
+    const bool warp_live = __any_sync(0xffffffffu, valid_q);
+    const int row = it.row0 + (valid_q ? q : 0) / G;
+    const int head = it.kv_head * G + (valid_q ? q : 0) % G;
+    // the query vector into fp16's range, and into the operand tile
+    float zf = 0.f;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(q_rot + (int64_t(row) * Hq + head) * D);
+      uint4 u[16];
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        u[i] = valid_q ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        float x[8];
+        unpack16<__nv_bfloat16>(u[i], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
+      }
+      const int up = fp8::query_exp(big);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float x[8];
+        unpack16<__nv_bfloat16>(u[i], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fp8::scale2(x[e], up);
+        *reinterpret_cast<uint4*>(S.q[t][i >> 3] + qm * 128 + (((i & 7) ^ (qm & 7)) << 4)) =
+            make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]),
+                       pack_half(x[6], x[7]));
+      }
+      zf = fp8::scale2(scale_log2, -up);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.q_full);
+    }
+    const int row_slot = valid_q ? m.slots[row] : INT_MAX;
+    const uint32_t* mrow =
+        mask_words && valid_q ? mask_words + m.mask_word_indptr[row] : nullptr;
+    const uint32_t lane_base = tmem + (uint32_t(quad * 32) << 16);
+    const uint32_t tO = lane_base + o_col<NT>(t);
+    float m_used = -INFINITY, l_run = 0.f;
+    for (int j = 0; j < T; ++j) {
+      const int ts = tile_at(j), st = j % NS;
+      const uint32_t tS = lane_base + s_col<NT>(t, j & 1);
+      uint32_t words[BN / 32];
+#pragma unroll
+      for (int i = 0; i < BN / 32; ++i)
+        words[i] = !mrow ? ~0u : (ts + 32 * i < ke ? mrow[(ts >> 5) + i] : 0u);
+      // (k_full: the converters' scales of the tile are this thread's to read)
+      if (!mbar_wait(&S.k_full[st], (j / NS) & 1) || !mbar_wait(&S.s_full[t][j & 1], (j >> 1) & 1)) {
+        bad = true;
+        break;
+      }
+      tc::fence_after();
+      if (warp_live) {
+        float s[BN];
+        ld64(tS, s);
+        bool all_vis;
+        if (mask_words) {
+          all_vis = ts + BN <= ke && (words[0] & words[1]) == ~0u;
+        } else {
+          // a tile's slots follow one another unless it holds the end of the
+          // sink pages
+          const int s0 = view.slot(ts), s1 = view.slot(ts + BN - 1);
+          all_vis = ts + BN <= ke && s1 - s0 == BN - 1 && s1 <= row_slot &&
+                    (view.window == 0 || s0 > row_slot - view.window || s1 < view.sinks);
+        }
+        if (!__all_sync(0xffffffffu, all_vis || !valid_q)) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c) {
+            const bool vis = valid_q && ts + c < ke &&
+                             (mask_words ? ((words[c >> 5] >> (c & 31)) & 1u) != 0
+                                         : view.sees(row_slot, view.slot(ts + c)));
+            s[c] = vis ? s[c] : -INFINITY;
+          }
+        }
+        // the largest x = zf 2^ek s + ev (zf > 0: the maximum of 8 slots of one
+        // page commutes with it)
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g8 = 0; g8 < BN / 8; ++g8) {
+          const float2 sc = *reinterpret_cast<const float2*>(&S.sc[st][g8]);
+          const float* e = s + 8 * g8;
+          const float m8 = max3(max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), fmaxf(e[6], e[7]));
+          mx = fmaxf(mx, fmaf(m8, zf * sc.x, sc.y));
+        }
+        float m_new = m_used;
+        if (m_used == -INFINITY || mx > m_used + 8.f) m_new = fmaxf(m_used, ceilf(mx));
+        const float alpha = m_new == m_used ? 1.f : ex2(m_used - m_new);
+        const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
+        float l_tile = 0.f;
+        uint32_t pk[BN / 2];
+#pragma unroll
+        for (int g8 = 0; g8 < BN / 8; ++g8) {
+          const float4 sc = S.sc[st][g8];
+          const float a = zf * sc.x, b = sc.y + neg_m;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x0, x1;
+            ffma2(x0, x1, s[8 * g8 + 2 * i], s[8 * g8 + 2 * i + 1], a, a, b, b);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            fadd2(sum0, sum1, p0, p1);
+            pk[4 * g8 + i] = pack_half(p0, p1);
+          }
+          l_tile = fmaf(sum0 + sum1, sc.z, l_tile);
+        }
+        l_run = fmaf(l_run, alpha, l_tile);
+        m_used = m_new;
+        st32(tS, pk);
+        // O is rescaled only after P.V of tile j - 1 has landed in it
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (!mbar_wait(&S.o_done[t][(j - 1) & 1], ((j - 1) >> 1) & 1)) {
+            bad = true;
+            break;
+          }
+          tc::fence_after();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float o[64];
+            ld64(tO + 64 * hh, o);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) o[c] *= alpha;
+            st64(tO + 64 * hh, o);
+          }
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[t][j & 1]);
+    }
+    if (warp_live && !bad) {
+      if (!mbar_wait(&S.o_done[t][(T - 1) & 1], ((T - 1) >> 1) & 1)) {
+        bad = true;
+      } else {
+        tc::fence_after();
+        const bool empty = !(l_run > 0.f);
+        const float inv = empty ? 0.f : 1.f / l_run;
+        const int rd0 = m.ro_indptr[row], rd1 = m.ro_indptr[row + 1];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float o[64];
+          ld64(tO + 64 * hh, o);
+          if (valid_q && it.direct) {
+            uint4 w[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[8 * c + e] *= inv;
+              w[c] = pack16<__nv_bfloat16>(o + 8 * c);
+            }
+            auto put = [&](__nv_bfloat16* base, int64_t r) {
+              uint4* dst = reinterpret_cast<uint4*>(base + (r * Hq + head) * D + 64 * hh);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) dst[c] = w[c];
+            };
+            if (out.out_all) put(out.out_all, row);
+            if (out.out_readout)
+              for (int i = rd0; i < rd1; ++i) put(out.out_readout, m.ro_idx[i]);
+          } else if (valid_q) {
+            float4* po = reinterpret_cast<float4*>(m.part_o + int64_t(it.part_base + q) * D + 64 * hh);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              po[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          }
+        }
+        if (valid_q) {
+          if (it.direct) {
+            const float lse = empty ? -INFINITY : (m_used + log2f(l_run)) * kLn2;
+            if (out.lse_all) out.lse_all[int64_t(row) * Hq + head] = lse;
+            if (out.lse_readout)
+              for (int i = rd0; i < rd1; ++i) out.lse_readout[int64_t(m.ro_idx[i]) * Hq + head] = lse;
+          } else {
+            m.part_ml[it.part_base + q] = make_float2(m_used, l_run);
+          }
+        }
+      }
+    }
+  }
+  if (T == 0) {
+    // nothing visible: empty states, or a direct item's zeros and -inf
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < nqv * 16; i += C::kThreads) {
+      const int q = i / 16, c = i % 16;
+      const int64_t row = it.row0 + q / G;
+      const int head = it.kv_head * G + q % G;
+      if (it.direct) {
+        auto put = [&](__nv_bfloat16* base, int64_t r) {
+          reinterpret_cast<uint4*>(base + (r * Hq + head) * D)[c] = zero;
+        };
+        if (out.out_all) put(out.out_all, row);
+        if (out.lse_all && c == 0) out.lse_all[row * Hq + head] = -INFINITY;
+        for (int k = m.ro_indptr[row]; k < m.ro_indptr[row + 1]; ++k) {
+          if (out.out_readout) put(out.out_readout, m.ro_idx[k]);
+          if (out.lse_readout && c == 0) out.lse_readout[int64_t(m.ro_idx[k]) * Hq + head] = -INFINITY;
+        }
+      } else {
+        float4* po = reinterpret_cast<float4*>(m.part_o + int64_t(it.part_base + q) * D);
+        po[2 * c] = po[2 * c + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c == 0) m.part_ml[it.part_base + q] = make_float2(-INFINITY, 0.f);
+      }
+    }
+  }
+  if (bad) set_status(status, PIE_STATUS_TIMEOUT);
+  tc::fence_before();
+  __syncthreads();
+  if (warp == C::kIssuer0 && all_tiles > 0) {
+    tc::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(C::kTmemCols)
+                 : "memory");
+  }
+}
+
+template <int NT>
+static cudaError_t launch_t8(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_scale,
+                             const uint8_t* v_scale, const uint32_t* mask_words, tc::Out out,
+                             uint32_t* status, const CUtensorMap& km, const CUtensorMap& vm,
+                             cudaStream_t s) {
+  const size_t smem = sizeof(t8::Smem<NT>) + 1024;
+  static_assert(sizeof(t8::Smem<NT>) + 1024 <= 227 * 1024, "shared memory of one SM");
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = set_smem_limit(attend_kv8_tc_kernel<NT>, int(smem), configured);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(attend_kv8_tc_kernel<NT>, dim3(p.num_tc_items), dim3(t8::Cfg<NT>::kThreads),
+                          smem, s, true, p.dev, p.G, p.desc.num_q_heads, p.desc.num_kv_heads,
+                          p.desc.page_size, p.desc.sm_scale * t8::kLog2e,
+                          static_cast<const __nv_bfloat16*>(q_rot), k_scale, v_scale, mask_words, out,
+                          status, km, vm);
+}
+
+cudaError_t launch_attend_kv8_tc(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_pool,
+                                 const uint8_t* v_pool, const uint8_t* k_scale,
+                                 const uint8_t* v_scale, const uint32_t* mask_words,
+                                 void* out_readout, float* lse_readout, void* out_all,
+                                 float* lse_all, uint32_t* status, cudaStream_t s) {
+  const int P = p.desc.page_size;
+  CUtensorMap km, vm;
+  const cuuint64_t dims[3] = {cuuint64_t(t8::D), cuuint64_t(P),
+                              cuuint64_t(p.dev.num_pool_pages) * p.desc.num_kv_heads};
+  const cuuint64_t str[2] = {cuuint64_t(t8::D), cuuint64_t(t8::D) * P};
+  const cuuint32_t box[3] = {cuuint32_t(t8::D), cuuint32_t(P), 1};
+  if (!tc::make_map(&km, k_pool, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+      !tc::make_map(&vm, v_pool, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_DATA_TYPE_UINT8))
+    return cudaErrorInvalidValue;
+  tc::Out out{static_cast<__nv_bfloat16*>(out_readout), lse_readout,
+              static_cast<__nv_bfloat16*>(out_all), lse_all};
+  return p.tc_nt == 2 ? launch_t8<2>(p, q_rot, k_scale, v_scale, mask_words, out, status, km, vm, s)
+                      : launch_t8<1>(p, q_rot, k_scale, v_scale, mask_words, out, status, km, vm, s);
+}
+
+}  // namespace pie

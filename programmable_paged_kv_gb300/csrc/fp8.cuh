@@ -38,5 +38,12 @@ __device__ __forceinline__ float scale2(float x, int e) {
   return x * pow2i(a) * pow2i(max(-252, min(252, e)) - a);
 }
 
+// the power of two that brings a query vector of largest magnitude `big` into
+// fp16's range (to [2^13, 2^14)); at most 2^100, so that its inverse times a
+// scale stays above zero: vectors below 2^-87 end lower in the range
+__device__ __forceinline__ int query_exp(float big) {
+  return min(100, 13 - (int(__float_as_uint(big) >> 23) - 127));
+}
+
 }  // namespace fp8
 }  // namespace pie

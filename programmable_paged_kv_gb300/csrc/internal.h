@@ -256,6 +256,11 @@ cudaError_t launch_attend_kv8(const pie_fwd_plan_t& p, const void* q_rot, const 
                               const uint8_t* v_pool, const uint8_t* k_scale,
                               const uint8_t* v_scale, const uint32_t* mask_words,
                               uint32_t* status, cudaStream_t s);
+cudaError_t launch_attend_kv8_tc(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_pool,
+                                 const uint8_t* v_pool, const uint8_t* k_scale,
+                                 const uint8_t* v_scale, const uint32_t* mask_words,
+                                 void* out_readout, float* lse_readout, void* out_all,
+                                 float* lse_all, uint32_t* status, cudaStream_t s);
 cudaError_t launch_combine(const pie_fwd_plan_t& p, void* out_readout, float* lse_readout,
                            void* out_all, float* lse_all, cudaStream_t s);
 

@@ -208,6 +208,8 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
       return fail(PIE_ERANGE, "window and sinks must not be negative");
     if (cache->sinks > 0 && cache->window == 0)
       return fail(PIE_EINVAL, "sinks without a window");
+    if (!(desc->sm_scale >= 0.0f && std::isfinite(desc->sm_scale)))
+      return fail(PIE_EINVAL, "sm_scale must be finite and not negative");
     if (cache->window > 0 && meta->mask_word_indptr)
       return fail(PIE_EINVAL, "a pass has a window or a mask, not both");
     H.kv8 = cache->kv_type == PIE_KV_E4M3;
@@ -387,6 +389,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   const bool tc_ok = D.dtype == PIE_BF16 && D.head_dim == 128 &&
                      kTcTileQueries % G == 0 &&
                      static_cast<int64_t>(M.num_pool_pages) * Hkv * D.page_size <= INT32_MAX;
+  const bool tc8_ok = D.dtype == PIE_BF16 && D.head_dim == 128 && kTcTileQueries % G == 0;
   // the tensor-core split-KV kernel (bf16, d 128, 32-bit tensor-copy rows);
   // the launch takes it under the same condition (decode_mma_supported)
   const int64_t pool_rows = static_cast<int64_t>(M.num_pool_pages) * Hkv * D.page_size;
@@ -400,14 +403,14 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   // split-KV kernel.
   auto lane_tc = [&](int l) {
     const int n = M.row_indptr[l + 1] - M.row_indptr[l];
-    if (H.kv8) return false;
+    if (H.kv8) return tc8_ok && n * G > 8;
     return tc_ok && n > 0 && (n * G >= kTcMinQueries || (H.has_mask && !mma_ok));
   };
   auto lane_list = [&](int l) { return !H.kv8 && H.has_mask && (lane_tc(l) || mma_ok); };
   // 8-bit caches: lanes with more query vectors per kv head than one item's 8
   // take wide items, which convert each code once for up to 32 of them
   auto lane_wide = [&](int l) {
-    return H.kv8 && (M.row_indptr[l + 1] - M.row_indptr[l]) * G > 8;
+    return H.kv8 && !lane_tc(l) && (M.row_indptr[l + 1] - M.row_indptr[l]) * G > 8;
   };
   const int wide_rows = std::max(1, kWideQueries / G);
   // split-KV items: chunk length from the total work
@@ -446,8 +449,10 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
     }
   }
   const int64_t tc_target = 4 * static_cast<int64_t>(H.sms);
-  const int64_t tc_ch = tc_units >= tc_target ? INT32_MAX
-                        : std::max<int64_t>(512, (tc_total + tc_target - 1) / tc_target);
+  int64_t tc_ch = tc_units >= tc_target ? INT32_MAX
+                  : std::max<int64_t>(512, (tc_total + tc_target - 1) / tc_target);
+  // (a masked item of an 8-bit cache lists its tiles in shared memory)
+  if (H.kv8 && H.has_mask) tc_ch = std::min<int64_t>(tc_ch, 65536);
   H.comb.clear();
   H.num_comb_merge = 0;
   H.row_block.assign(N, 0);
@@ -924,8 +929,11 @@ int pie_fwd_attend_kv8(const pie_fwd_plan_t* plan, const void* q_rot, const uint
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (g_ev_start) e = cudaEventRecord(g_ev_start, s);
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && plan->num_dec_items + plan->num_wide_items > 0)
     e = launch_attend_kv8(*plan, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words, status, s);
+  if (e == cudaSuccess && plan->num_tc_items > 0)
+    e = launch_attend_kv8_tc(*plan, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words,
+                             out_readout, lse_readout, out_all, lse_all, status, s);
   if (e == cudaSuccess && g_ev_stop) e = cudaEventRecord(g_ev_stop, s);
   if (e == cudaSuccess && plan->num_comb_merge > 0)
     e = launch_combine(*plan, out_readout, lse_readout, out_all, lse_all, s);
