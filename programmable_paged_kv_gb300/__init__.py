@@ -132,24 +132,24 @@ def forward_cache(desc: abi.pie_fwd_desc, cache: abi.pie_fwd_cache, meta: _HostM
     given cache in one native call; k_scale and v_scale belong to an e4m3
     cache.  workspace: as in forward(), sized by workspace_bytes(desc, meta,
     cache)."""
-    if cache.kv_type == PIE_KV_E4M3:
-        _check_kv8(desc, k_pool, v_pool, k_scale, v_scale, int(meta.c.num_pool_pages))
-    dt = _torch_dtype(desc)
-    rows = _check_rows(desc, int(meta.c.num_rows), q=q, q_rot=q_rot, out_all=out_all)
-    _check_kv_rows(desc, rows, k=k, v=v)
-    _same_device(workspace, q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale, frozen_len,
-                 mask_words, out_readout, lse_readout, out_all, lse_all, channel, status)
-    if out_readout is not None and out_readout.dtype != dt:
-        raise ValueError(f"out_readout must be {dt}")
+    kv8 = cache.kv_type == PIE_KV_E4M3
+    if kv8 and (k_scale is None or v_scale is None):
+        raise ValueError("an e4m3 cache needs k_scale and v_scale")
+    c = meta.c
+    # (readouts by default: the last row of every lane that has rows)
+    n_ro = c.num_readout if c.readout else int(np.count_nonzero(np.diff(meta.keep["row_indptr"])))
+    z, p = _Shapes(desc, c, n_ro), _Args(stream)
+    pool = 1 if kv8 else z.dt
     abi.check(abi.load().pie_fwd_forward_cache(
-        C.byref(desc), C.byref(cache), C.byref(meta.c), _ptr(workspace, "workspace"),
-        workspace.numel(), _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(q_rot, "q_rot"),
-        _ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"), _ptr(k_scale, "k_scale", False),
-        _ptr(v_scale, "v_scale", False), _ptr(frozen_len, "frozen_len"),
-        _ptr(mask_words, "mask_words", False), _ptr(out_readout, "out_readout", False),
-        _ptr(lse_readout, "lse_readout", False), _ptr(out_all, "out_all", False),
-        _ptr(lse_all, "lse_all", False), _ptr(channel, "channel", False),
-        _ptr(status, "status", False), _stream(stream)), "pie_fwd_forward_cache")
+        C.byref(desc), C.byref(cache), C.byref(c), p(workspace, "workspace", None, 1),
+        workspace.numel(), p(q, "q", z.q, z.dt), p(k, "k", z.kv, z.dt), p(v, "v", z.kv, z.dt),
+        p(q_rot, "q_rot", z.q, z.dt), p(k_pool, "k_pool", z.pool, pool),
+        p(v_pool, "v_pool", z.pool, pool), p(k_scale, "k_scale", z.scale, 1),
+        p(v_scale, "v_scale", z.scale, 1), p(frozen_len, "frozen_len", z.lanes, z.i32),
+        p(mask_words, "mask_words", None, 4), p(out_readout, "out_readout", z.ro, z.dt),
+        p(lse_readout, "lse_readout", z.ro_lse, z.f32), p(out_all, "out_all", z.q, z.dt),
+        p(lse_all, "lse_all", z.lse, z.f32), p(channel, "channel", z.lanes, z.i32),
+        p(status, "status", None, 4), p.stream), "pie_fwd_forward_cache")
 
 
 def copy_pages(pools, src, dst, status=None, stream=None) -> None:
@@ -158,28 +158,28 @@ def copy_pages(pools, src, dst, status=None, stream=None) -> None:
     same pages: the K, V and scale pools of a model's layers); src and dst are
     int32 CUDA tensors of one length."""
     import torch
-    pools = list(pools)
-    if not pools:
-        return
-    pages = int(pools[0].shape[0])
+    p = _Args(stream)
+    n_pairs = src.numel()
+    line = torch.Size((n_pairs,))
+    src_p, dst_p = p(src, "src", line, torch.int32), p(dst, "dst", line, torch.int32)
+    status_p = p(status, "status", None, 4)
+    ptrs, sizes, pages = [], [], None
     for t in pools:
-        if t.dim() < 1 or int(t.shape[0]) != pages:
+        n = t.shape[0] if t.dim() else -1
+        if pages is None:
+            pages = n
+        if n != pages or n < 0:
             raise ValueError("the pools must have the same number of pages")
-    for t, what in ((src, "src"), (dst, "dst")):
-        if t.dtype != torch.int32 or t.dim() != 1:
-            raise ValueError(f"{what} must be a 1-D int32 tensor")
-    if src.numel() != dst.numel():
-        raise ValueError("src and dst must have one length")
-    _same_device(src, dst, status, *pools)
-    if pages == 0 or src.numel() == 0:
+        ptr = p(t, "pool")
+        if t.nbytes:  # (a pool whose pages hold nothing has nothing to copy)
+            ptrs.append(ptr)
+            sizes.append(t.nbytes // n)
+    if not ptrs or n_pairs == 0:
         return
-    keep = [t for t in pools if t.numel()]
-    n = len(keep)
-    ptrs = (C.c_void_p * max(n, 1))(*[_ptr(t, "pool") for t in keep])
-    size = (C.c_int64 * max(n, 1))(*[t.numel() // pages * t.element_size() for t in keep])
-    abi.check(abi.load().pie_fwd_copy_pages(n, ptrs, size, pages, src.numel(), _ptr(src, "src"),
-                                            _ptr(dst, "dst"), _ptr(status, "status", False),
-                                            _stream(stream)), "pie_fwd_copy_pages")
+    ptrs, sizes = np.array(ptrs, np.uint64), np.array(sizes, np.int64)
+    abi.check(abi.load().pie_fwd_copy_pages(ptrs.size, ptrs.ctypes.data, sizes.ctypes.data, pages,
+                                            n_pairs, src_p, dst_p, status_p, p.stream),
+              "pie_fwd_copy_pages")
 
 
 def decode_loop_workspace_bytes(desc: abi.pie_fwd_desc, num_lanes: int, max_pages_per_lane: int) -> int:
@@ -250,43 +250,54 @@ def _ptr(t, what: str, required: bool = True):
     return t.data_ptr()
 
 
-def _same_device(*tensors) -> None:
-    """Every tensor given lives on the current device (the launches go there)."""
-    import torch
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != here):
-            raise ValueError("every tensor must be on the current CUDA device")
+class _Args:
+    """Device addresses of one call's tensors, checked on the way: on the device
+    the call launches on (the current one), contiguous, of the shape and type
+    that the plan implies.  (One attribute read per check: a decode step's
+    calls take a few microseconds on the GPU.)"""
+
+    __slots__ = ("stream", "device")
+
+    def __init__(self, stream):
+        import torch
+        here = torch.cuda.current_stream()
+        self.device = here.device_index
+        if stream is None:
+            stream = here
+        elif stream.device_index != self.device:
+            raise ValueError("the stream must belong to the current CUDA device")
+        self.stream = stream.cuda_stream
+
+    def __call__(self, t, what: str, shape=None, dtype=None):
+        if t is None:
+            return None
+        if t.get_device() != self.device:
+            raise ValueError(f"{what} must be a tensor on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        # dtype: a torch dtype, or 1 for any one-byte type and 4 for any four-byte one
+        if dtype is not None and t.dtype != dtype and t.element_size() != dtype:
+            raise ValueError(f"{what} must be of type {dtype} (a number: bytes per element)")
+        return t.data_ptr()
 
 
-def _torch_dtype(desc):
-    import torch
-    return torch.bfloat16 if desc.dtype == PIE_BF16 else torch.float32
+class _Shapes:
+    """The shapes and types of a pass's tensors, made once per plan."""
 
-
-def _check_rows(desc, rows: int, **tensors) -> int:
-    """Query-shaped tensors: [rows, num_q_heads, head_dim] of the pass dtype."""
-    want = (rows, desc.num_q_heads, desc.head_dim)
-    for what, t in tensors.items():
-        if t is not None and (tuple(t.shape) != want or t.dtype != _torch_dtype(desc)):
-            raise ValueError(f"{what} must be {want} of {_torch_dtype(desc)}")
-    return rows
-
-
-def _check_kv_rows(desc, rows: int, **tensors) -> None:
-    want = (rows, desc.num_kv_heads, desc.head_dim)
-    for what, t in tensors.items():
-        if tuple(t.shape) != want or t.dtype != _torch_dtype(desc):
-            raise ValueError(f"{what} must be {want} of {_torch_dtype(desc)}")
-
-
-def _check_kv8(desc, k_pool, v_pool, k_scale, v_scale, pages: int) -> None:
-    """Pools of codes [pages, Hkv, P, d] and scales [pages, Hkv], one byte each."""
-    shape = (pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
-    for what, t, want in (("k_pool", k_pool, shape), ("v_pool", v_pool, shape),
-                          ("k_scale", k_scale, shape[:2]), ("v_scale", v_scale, shape[:2])):
-        if t is None or tuple(t.shape) != want or t.element_size() != 1:
-            raise ValueError(f"{what} must be {want} of one byte each")
+    def __init__(self, desc, c, num_readout: int):
+        import torch
+        size = torch.Size
+        N, Hq, Hkv, d = c.num_rows, desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+        self.dt = torch.bfloat16 if desc.dtype == PIE_BF16 else torch.float32
+        self.f32, self.i32 = torch.float32, torch.int32
+        self.q, self.kv = size((N, Hq, d)), size((N, Hkv, d))
+        self.lse = size((N, Hq))
+        self.ro, self.ro_lse = size((num_readout, Hq, d)), size((num_readout, Hq))
+        self.pool = size((c.num_pool_pages, Hkv, desc.page_size, d))
+        self.scale = size((c.num_pool_pages, Hkv))
+        self.lanes = size((c.num_lanes,))
 
 
 def _stream(stream):
@@ -324,6 +335,7 @@ class ForwardPlan:
             "pie_fwd_plan")
         self.handle = h
         self.num_readout = int(self.lib.pie_fwd_plan_num_readout(h))
+        self._shapes = _Shapes(desc, meta.c, self.num_readout) if cache is not None else None
 
     @classmethod
     def _adopt(cls, handle, desc: abi.pie_fwd_desc, workspace):
@@ -336,7 +348,13 @@ class ForwardPlan:
         self.workspace = workspace
         self.handle = handle
         self.num_readout = int(self.lib.pie_fwd_plan_num_readout(handle))
+        self._shapes = None  # (a plan of the pass dtype)
         return self
+
+    def _kv8_shapes(self) -> "_Shapes":
+        if self._shapes is None:
+            raise ValueError("the plan was made without a cache (see make_cache)")
+        return self._shapes
 
     def append_kv(self, q, k, v, q_rot, k_pool, v_pool, frozen_len, status=None, stream=None):
         abi.check(self.lib.pie_fwd_append_kv(
@@ -363,32 +381,26 @@ class ForwardPlan:
                    stream=None):
         """pie_fwd_append_kv8: k_pool / v_pool [pages, Hkv, P, d] e4m3 codes (any
         1-byte dtype), k_scale / v_scale [pages, Hkv] E8M0 bytes."""
-        rows = _check_rows(self.desc, int(self.meta.c.num_rows), q=q, q_rot=q_rot)
-        _check_kv_rows(self.desc, rows, k=k, v=v)
-        _check_kv8(self.desc, k_pool, v_pool, k_scale, v_scale, int(self.meta.c.num_pool_pages))
-        _same_device(q, k, v, q_rot, k_pool, v_pool, k_scale, v_scale, frozen_len, status)
+        z, p = self._kv8_shapes(), _Args(stream)
         abi.check(self.lib.pie_fwd_append_kv8(
-            self.handle, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(q_rot, "q_rot"),
-            _ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"), _ptr(k_scale, "k_scale"),
-            _ptr(v_scale, "v_scale"), _ptr(frozen_len, "frozen_len"),
-            _ptr(status, "status", False), _stream(stream)), "pie_fwd_append_kv8")
+            self.handle, p(q, "q", z.q, z.dt), p(k, "k", z.kv, z.dt), p(v, "v", z.kv, z.dt),
+            p(q_rot, "q_rot", z.q, z.dt), p(k_pool, "k_pool", z.pool, 1),
+            p(v_pool, "v_pool", z.pool, 1), p(k_scale, "k_scale", z.scale, 1),
+            p(v_scale, "v_scale", z.scale, 1), p(frozen_len, "frozen_len", z.lanes, z.i32),
+            p(status, "status", None, 4), p.stream), "pie_fwd_append_kv8")
 
     def attend_kv8(self, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words=None,
                    out_readout=None, lse_readout=None, out_all=None, lse_all=None, status=None,
                    stream=None):
         """pie_fwd_attend_kv8: attend() over the codes and scales of append_kv8."""
-        rows = _check_rows(self.desc, int(self.meta.c.num_rows), q_rot=q_rot, out_all=out_all)
-        _check_rows(self.desc, self.num_readout, out_readout=out_readout)
-        _check_kv8(self.desc, k_pool, v_pool, k_scale, v_scale, int(self.meta.c.num_pool_pages))
-        _same_device(q_rot, k_pool, v_pool, k_scale, v_scale, mask_words, out_readout, lse_readout,
-                     out_all, lse_all, status)
+        z, p = self._kv8_shapes(), _Args(stream)
         abi.check(self.lib.pie_fwd_attend_kv8(
-            self.handle, _ptr(q_rot, "q_rot"), _ptr(k_pool, "k_pool"), _ptr(v_pool, "v_pool"),
-            _ptr(k_scale, "k_scale"), _ptr(v_scale, "v_scale"),
-            _ptr(mask_words, "mask_words", False), _ptr(out_readout, "out_readout", False),
-            _ptr(lse_readout, "lse_readout", False), _ptr(out_all, "out_all", False),
-            _ptr(lse_all, "lse_all", False), _ptr(status, "status", False), _stream(stream)),
-            "pie_fwd_attend_kv8")
+            self.handle, p(q_rot, "q_rot", z.q, z.dt), p(k_pool, "k_pool", z.pool, 1),
+            p(v_pool, "v_pool", z.pool, 1), p(k_scale, "k_scale", z.scale, 1),
+            p(v_scale, "v_scale", z.scale, 1), p(mask_words, "mask_words", None, 4),
+            p(out_readout, "out_readout", z.ro, z.dt), p(lse_readout, "lse_readout", z.ro_lse, z.f32),
+            p(out_all, "out_all", z.q, z.dt), p(lse_all, "lse_all", z.lse, z.f32),
+            p(status, "status", None, 4), p.stream), "pie_fwd_attend_kv8")
 
     def fold(self, frozen_len, channel=None, status=None, stream=None):
         abi.check(self.lib.pie_fwd_fold(

@@ -4,12 +4,15 @@
 //
 // One page is one unit: its slots share their scales, so the rows of the pass
 // that write it (the plan's WriteBlock) are quantised together with the page's
-// live codes.  One warp takes one kv head of one page, K and V, and the query
-// heads of its group for the same rows; the warps of a CTA share the rows'
-// rotation angles.  The scale is a power of two: e4m3 is a floating format, so
-// a finer scale would buy no precision, products with it are exact, and a page
-// whose scale grows shifts its codes' exponents (only values that fall under
-// e4m3's smallest normal lose bits).  A page's codes are read only then.
+// live codes.  The scale is a power of two: e4m3 is a floating format, so a finer
+// scale would buy no precision, products with it are exact, and a page whose
+// scale grows shifts its codes' exponents (only values that fall under e4m3's
+// smallest normal lose bits).  A page's codes are read only then.
+// Three kinds of CTAs per page, 8 warps each: K (a warp per kv head, which holds
+// the head's rows of the page in registers between finding the scale and writing
+// the codes; the rows' rotation angles are shared), V (the same without a
+// rotation), and the rows' query heads.  All global accesses are 16-byte vectors
+// of a row, a warp's worth of rows in flight at once.
 //
 // A code is the nearest to the exactly rotated value, so it does not depend on
 // how the rotation was evaluated:
@@ -31,7 +34,8 @@ namespace pie {
 
 namespace ak {
 
-constexpr int WARPS = 4;
+constexpr int WARPS = 8, THREADS = 32 * WARPS;
+constexpr int QUNITS = 128;  // (row, query head) units per query CTA
 
 // cos and sin of 2 pi t / 2^64, each as a sum of two floats
 struct Angle {
@@ -125,186 +129,215 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void load_n(const T* p, float* f) {
-  if constexpr (sizeof(T) * N == 16) {
-    unpack16<T>(*reinterpret_cast<const uint4*>(p), f);
-  } else if constexpr (sizeof(T) * N == 8) {
-    unpack8<T>(*reinterpret_cast<const uint2*>(p), f);
-  } else if constexpr (sizeof(T) * N == 4 && N == 2) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-    f[0] = __uint_as_float(u << 16);
-    f[1] = __uint_as_float(u & 0xFFFF0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(p[i]);
-  }
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_n(T* p, const float* f) {
-  if constexpr (sizeof(T) == 2 && N == 2) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(f[0], f[1]);
-    *reinterpret_cast<__nv_bfloat162*>(p) = h;
-  } else if constexpr (sizeof(T) == 4 && N == 2) {
-    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = Elem<T>::from_f(f[i]);
-  }
-}
+// N codes (4 or 8) of consecutive elements
 template <int N>
 __device__ __forceinline__ void store_codes(uint8_t* p, const float* f) {
-  if constexpr (N == 4)
-    *reinterpret_cast<uint32_t*>(p) =
-        fp8::from_float2(f[0], f[1]) | (fp8::from_float2(f[2], f[3]) << 16);
-  else if constexpr (N == 2)
-    *reinterpret_cast<uint16_t*>(p) = uint16_t(fp8::from_float2(f[0], f[1]));
-  else
-    *p = uint8_t(fp8::from_float2(f[0], 0.f));
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    w[i] = fp8::from_float2(f[4 * i], f[4 * i + 1]) | (fp8::from_float2(f[4 * i + 2], f[4 * i + 3]) << 16);
+  if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
 // The page's live codes of one kv head (rows of D bytes, offsets `keep`) from
 // scale 2^old to 2^e.
 template <int D>
 __device__ __forceinline__ void regrow(uint8_t* rows, uint32_t keep, int old, int e, int lane) {
-  constexpr int N = D / 32;  // codes per lane
-  const int diff = old - e;  // < 0
-  while (keep) {
-    const int o = __ffs(keep) - 1;
-    keep &= keep - 1;
-    uint8_t* p = rows + o * D + lane * N;
-    const uint32_t c = N == 4 ? *reinterpret_cast<const uint32_t*>(p)
-                              : uint32_t(*reinterpret_cast<const uint16_t*>(p));
-    uint32_t h[2];
-    fp8::to_half2x2(c, h[0], h[1]);
-    float f[4];
+  constexpr int LPR = D / 16;  // lanes per row, 16 codes each
+  const int diff = old - e;    // < 0
+  for (int o = lane / LPR; o < 32; o += 32 / LPR) {
+    if (!((keep >> o) & 1u)) continue;
+    uint4* p = reinterpret_cast<uint4*>(rows + o * D + (lane % LPR) * 16);
+    const uint4 c = *p;
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    uint32_t out[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      f[2 * i] = fp8::scale2(v.x, diff);
-      f[2 * i + 1] = fp8::scale2(v.y, diff);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[2];
+      fp8::to_half2x2(in[i], h[0], h[1]);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+      out[i] = fp8::from_float2(fp8::scale2(a.x, diff), fp8::scale2(a.y, diff)) |
+               (fp8::from_float2(fp8::scale2(b.x, diff), fp8::scale2(b.y, diff)) << 16);
     }
-    store_codes<N>(p, f);
+    *p = make_uint4(out[0], out[1], out[2], out[3]);
   }
+}
+
+// One head's rows of a page, from the floats `x` that lane (row, c) holds of row
+// i = it * RPI + lane / (32 / RPI): find the exponent, move the live codes, write
+// `put(it, exponent)` for every row that is written.
+template <int D, int ITS, int RPI, int N, typename Put>
+__device__ __forceinline__ void quantise(float (&x)[ITS][N], const bool (&mine)[ITS], uint8_t* codes,
+                                         uint8_t* scale, uint32_t keep, int lane, Put put) {
+  float amax = 0.f;
+#pragma unroll
+  for (int it = 0; it < ITS; ++it)
+    if (mine[it])
+#pragma unroll
+      for (int e = 0; e < N; ++e) amax = fmaxf(amax, fabsf(x[it][e]));
+  const int old = int(*scale) - fp8::kBias;
+  int ex = needed_exp(warp_max(amax));
+  if (keep) {
+    ex = max(ex, old);
+    if (ex > old) regrow<D>(codes, keep, old, ex, lane);
+  }
+  __syncwarp();  // every lane has read the old scale
+  if (lane == 0) *scale = uint8_t(ex + fp8::kBias);
+#pragma unroll
+  for (int it = 0; it < ITS; ++it)
+    if (mine[it]) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[it][e] = fp8::scale2(x[it][e], -ex);
+      put(it);
+    }
 }
 
 }  // namespace ak
 
-template <typename T, int D>
-__global__ void __launch_bounds__(ak::WARPS * 32) append_kv8_kernel(
-    DevMeta m, int Hq, int Hkv, int P, const T* q, const T* k, const T* v, T* q_rot,
+// MAXR: the most rows one page holds (16 or 32).
+template <typename T, int D, int MAXR>
+__global__ void __launch_bounds__(ak::THREADS) append_kv8_kernel(
+    DevMeta m, int Hq, int Hkv, int P, int head_ctas, const T* q, const T* k, const T* v, T* q_rot,
     uint8_t* k_pool, uint8_t* v_pool, uint8_t* k_scale, uint8_t* v_scale,
     const int32_t* frozen_len, uint32_t* status) {
   using namespace ak;
   constexpr int H = D / 2;
-  constexpr int PL = H / 32;  // rotation pairs per lane: elements i0 .. and H + i0 ..
-  constexpr int VL = D / 32;  // V elements per lane
-  extern __shared__ Angle ang[];  // [rows of the page][H]
+  constexpr int VEC = 16 / sizeof(T);  // elements per 16-byte vector
+  constexpr int UL = H / VEC;          // lanes per rotated row: c holds elements c VEC .. of both halves
+  // angle e of vector c of row i: neighbouring lanes' angles side by side
+  extern __shared__ Angle ang[];  // [rows][VEC][UL]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the plan's own data (uploaded before any kernel of the pass) and the
-  // angles, while the kernel before this one may still run
   const WriteBlock wb = m.wblocks[blockIdx.x];
   const int32_t* rows = m.wrow + wb.row0;
-  for (int i = threadIdx.x; i < wb.nrows * H; i += WARPS * 32)
-    ang[i] = angle(uint64_t(uint32_t(m.positions[rows[i / H]])) * m.rope_turn[i % H]);
+  const int part = int(blockIdx.y);
+  const bool is_k = part < head_ctas, is_v = !is_k && part < 2 * head_ctas;
+  // query CTAs: kQUnits (row, head) units each
+  const int unit0 = is_k || is_v ? 0 : (part - 2 * head_ctas) * QUNITS;
+  const int units = is_k || is_v ? 0 : min(QUNITS, wb.nrows * Hq - unit0);
+  if (!is_k && !is_v && units <= 0) return;
+  // the angles come from the plan's own data (uploaded before any kernel of the
+  // pass): while the kernel before this one may still run
+  const int ang0 = is_k ? 0 : unit0 / Hq, ang1 = is_k ? wb.nrows : is_v ? 0 : (unit0 + units - 1) / Hq + 1;
+  for (int j = threadIdx.x; j < (ang1 - ang0) * H; j += THREADS) {
+    const int i = j / H, f = j % H;
+    const uint64_t turns = uint64_t(uint32_t(m.positions[rows[ang0 + i]])) * m.rope_turn[f];
+    Angle& a = ang[i * H + (f % VEC) * UL + f / VEC];
+    if (is_k) {
+      a = angle(turns);
+    } else {
+      // queries are rounded to the pass dtype: fp32 sine and cosine of the
+      // signed fraction of a turn (2^-32 turns apart) serve
+      float s, c;
+      sincospif(float(int32_t(turns >> 32)) * 0x1p-31f, &s, &c);
+      a.ch = c;
+      a.sh = s;
+    }
+  }
   const int slot0 = wb.lpage * P;
   const int kv_len = m.kv_len[wb.lane];
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
+
+  if (!is_k && !is_v) {
+    // ---- query heads, frozen rows included
+    for (int j = threadIdx.x; j < units * UL; j += THREADS) {
+      const int u = unit0 + j / UL, c = j % UL;
+      const int i = u / Hq;
+      const int64_t at = (int64_t(rows[i]) * Hq + u % Hq) * D + c * VEC;
+      float x[VEC], y[VEC], lo[VEC], hi[VEC];
+      unpack16<T>(*reinterpret_cast<const uint4*>(q + at), x);
+      unpack16<T>(*reinterpret_cast<const uint4*>(q + at + H), y);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const Angle& a = ang[(i - ang0) * H + e * UL + c];
+        lo[e] = fmaf(x[e], a.ch, -(y[e] * a.sh));
+        hi[e] = fmaf(y[e], a.ch, x[e] * a.sh);
+      }
+      *reinterpret_cast<uint4*>(q_rot + at) = pack16<T>(lo);
+      *reinterpret_cast<uint4*>(q_rot + at + H) = pack16<T>(hi);
+    }
+    return;
+  }
+
   const int frozen = frozen_len[wb.lane];
-  if (blockIdx.y == 0 && threadIdx.x < wb.nrows) {
+  if (part == 0 && threadIdx.x < wb.nrows) {
     const int r = rows[threadIdx.x], slot = m.slots[r];
     if (slot < frozen) set_status(status, PIE_STATUS_FROZEN_WRITE);
     if (r == m.row_indptr[wb.lane] && m.fold_mode[wb.lane] != PIE_FOLD_NONE && slot != frozen)
       set_status(status, PIE_STATUS_FOLD_GAP);
   }
-  const int g = blockIdx.y * WARPS + warp;
+  const int g = (is_k ? part : part - head_ctas) * WARPS + warp;
   if (g >= Hkv) return;
-  const int G = Hq / Hkv;
-  const int i0 = lane * PL;
-
-  // ---- K and V: the slots written now, the live ones that stay
+  // the slots written now, and the live ones that stay
   const bool wr = lane < P && ((wb.written >> lane) & 1u) && slot0 + lane >= frozen;
   const bool live = lane < P && slot0 + lane < max(kv_len, frozen);
   const uint32_t writes = __ballot_sync(0xffffffffu, wr);
   const uint32_t keep = __ballot_sync(0xffffffffu, live && !wr);
-  if (writes) {
-    const int64_t cell = int64_t(wb.page) * Hkv + g;
-    auto rotated = [&](int i, float* lo, float* hi) {  // row i of the page, this lane's pairs
-      const T* src = k + (int64_t(rows[i]) * Hkv + g) * D;
-      float x[PL], y[PL];
-      load_n<T, PL>(src + i0, x);
-      load_n<T, PL>(src + H + i0, y);
-#pragma unroll
-      for (int e = 0; e < PL; ++e) {
-        const Angle a = ang[i * H + i0 + e];
-        lo[e] = rot_odd(x[e], a.ch, a.cl, y[e], a.sh, a.sl);
-        hi[e] = rot_odd(y[e], a.ch, a.cl, -x[e], a.sh, a.sl);
-      }
-    };
-    float ka = 0.f, va = 0.f;
-    for (int i = 0; i < wb.nrows; ++i) {
-      const int r = rows[i];
-      if (m.slots[r] < frozen) continue;
-      float lo[PL], hi[PL], f[VL];
-      rotated(i, lo, hi);
-      load_n<T, VL>(v + (int64_t(r) * Hkv + g) * D + lane * VL, f);
-#pragma unroll
-      for (int e = 0; e < PL; ++e) ka = fmaxf(ka, fmaxf(fabsf(lo[e]), fabsf(hi[e])));
-#pragma unroll
-      for (int e = 0; e < VL; ++e) va = fmaxf(va, fabsf(f[e]));
-    }
-    const int k_old = int(k_scale[cell]) - fp8::kBias, v_old = int(v_scale[cell]) - fp8::kBias;
-    int ke = needed_exp(warp_max(ka)), ve = needed_exp(warp_max(va));
-    uint8_t* kc = k_pool + cell * P * D;
-    uint8_t* vc = v_pool + cell * P * D;
-    if (keep) {
-      ke = max(ke, k_old);
-      ve = max(ve, v_old);
-      if (ke > k_old) regrow<D>(kc, keep, k_old, ke, lane);
-      if (ve > v_old) regrow<D>(vc, keep, v_old, ve, lane);
-    }
-    __syncwarp();  // every lane has read the old scales
-    if (lane == 0) {
-      k_scale[cell] = uint8_t(ke + fp8::kBias);
-      v_scale[cell] = uint8_t(ve + fp8::kBias);
-    }
-    for (int i = 0; i < wb.nrows; ++i) {
-      const int r = rows[i], slot = m.slots[r];
-      if (slot < frozen) continue;
-      const int o = (slot - slot0) * D;
-      float lo[PL], hi[PL], f[VL];
-      rotated(i, lo, hi);
-#pragma unroll
-      for (int e = 0; e < PL; ++e) {
-        lo[e] = fp8::scale2(lo[e], -ke);
-        hi[e] = fp8::scale2(hi[e], -ke);
-      }
-      store_codes<PL>(kc + o + i0, lo);
-      store_codes<PL>(kc + o + H + i0, hi);
-      load_n<T, VL>(v + (int64_t(r) * Hkv + g) * D + lane * VL, f);
-#pragma unroll
-      for (int e = 0; e < VL; ++e) f[e] = fp8::scale2(f[e], -ve);
-      store_codes<VL>(vc + o + lane * VL, f);
-    }
-  }
+  if (!writes) return;
+  const int64_t cell = int64_t(wb.page) * Hkv + g;
 
-  // ---- the group's query heads, frozen rows included
-  for (int u = 0; u < wb.nrows * G; ++u) {
-    const int i = u / G;
-    const int64_t at = (int64_t(rows[i]) * Hq + g * G + u % G) * D;
-    float x[PL], y[PL], lo[PL], hi[PL];
-    load_n<T, PL>(q + at + i0, x);
-    load_n<T, PL>(q + at + H + i0, y);
+  if (is_k) {
+    constexpr int RPI = 32 / UL, ITS = MAXR / RPI;  // rows per step, steps
+    const int c = lane % UL;
+    uint8_t* codes = k_pool + cell * P * D;
+    float x[ITS][2 * VEC];  // the rotated row's low part, then its high part
+    bool mine[ITS];
+    int off[ITS];
+    uint4 raw[ITS][2];
 #pragma unroll
-    for (int e = 0; e < PL; ++e) {
-      const Angle a = ang[i * H + i0 + e];
-      lo[e] = fmaf(x[e], a.ch, -(y[e] * a.sh));
-      hi[e] = fmaf(y[e], a.ch, x[e] * a.sh);
+    for (int it = 0; it < ITS; ++it) {
+      const int i = it * RPI + lane / UL;
+      const int r = i < wb.nrows ? rows[i] : rows[0];
+      const int slot = m.slots[r];
+      off[it] = slot - slot0;
+      mine[it] = i < wb.nrows && slot >= frozen;
+      if (mine[it]) {
+        const T* src = k + (int64_t(r) * Hkv + g) * D + c * VEC;
+        raw[it][0] = *reinterpret_cast<const uint4*>(src);
+        raw[it][1] = *reinterpret_cast<const uint4*>(src + H);
+      }
     }
-    store_n<T, PL>(q_rot + at + i0, lo);
-    store_n<T, PL>(q_rot + at + H + i0, hi);
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) {
+      if (!mine[it]) continue;
+      const int i = it * RPI + lane / UL;
+      float a[VEC], b[VEC];
+      unpack16<T>(raw[it][0], a);
+      unpack16<T>(raw[it][1], b);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const Angle t = ang[i * H + e * UL + c];
+        x[it][e] = rot_odd(a[e], t.ch, t.cl, b[e], t.sh, t.sl);
+        x[it][VEC + e] = rot_odd(b[e], t.ch, t.cl, -a[e], t.sh, t.sl);
+      }
+    }
+    quantise<D, ITS, RPI, 2 * VEC>(x, mine, codes, k_scale + cell, keep, lane, [&](int it) {
+      store_codes<VEC>(codes + off[it] * D + c * VEC, x[it]);
+      store_codes<VEC>(codes + off[it] * D + H + c * VEC, x[it] + VEC);
+    });
+  } else {
+    constexpr int VLN = D / VEC, RPI = 32 / VLN, ITS = MAXR / RPI;
+    const int c = lane % VLN;
+    uint8_t* codes = v_pool + cell * P * D;
+    float x[ITS][VEC];
+    bool mine[ITS];
+    int off[ITS];
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) {
+      const int i = it * RPI + lane / VLN;
+      const int r = i < wb.nrows ? rows[i] : rows[0];
+      const int slot = m.slots[r];
+      off[it] = slot - slot0;
+      mine[it] = i < wb.nrows && slot >= frozen;
+      if (mine[it])
+        unpack16<T>(*reinterpret_cast<const uint4*>(v + (int64_t(r) * Hkv + g) * D + c * VEC), x[it]);
+    }
+    quantise<D, ITS, RPI, VEC>(x, mine, codes, v_scale + cell, keep, lane, [&](int it) {
+      store_codes<VEC>(codes + off[it] * D + c * VEC, x[it]);
+    });
   }
 }
 
@@ -313,13 +346,16 @@ static cudaError_t launch_ak(const pie_fwd_plan_t& p, const void* q, const void*
                              void* q_rot, uint8_t* k_pool, uint8_t* v_pool, uint8_t* k_scale,
                              uint8_t* v_scale, const int32_t* frozen, uint32_t* status,
                              cudaStream_t s) {
-  const int Hkv = p.desc.num_kv_heads;
-  const dim3 grid(p.num_wblocks, (Hkv + ak::WARPS - 1) / ak::WARPS);
-  const size_t smem = size_t(p.desc.page_size) * (D / 2) * sizeof(ak::Angle);  // at most 32 KB
-  return launch_dependent(append_kv8_kernel<T, D>, grid, dim3(ak::WARPS * 32), smem, s, true, p.dev,
-                          p.desc.num_q_heads, Hkv, p.desc.page_size, static_cast<const T*>(q),
-                          static_cast<const T*>(k), static_cast<const T*>(v),
-                          static_cast<T*>(q_rot), k_pool, v_pool, k_scale, v_scale, frozen, status);
+  const int Hq = p.desc.num_q_heads, Hkv = p.desc.num_kv_heads, P = p.desc.page_size;
+  const int heads = (Hkv + ak::WARPS - 1) / ak::WARPS;
+  const int queries = (p.max_wrows * Hq + ak::QUNITS - 1) / ak::QUNITS;
+  const dim3 grid(p.num_wblocks, 2 * heads + queries);
+  const size_t smem = size_t(p.max_wrows) * (D / 2) * sizeof(ak::Angle);  // at most 32 KB
+  auto f = p.max_wrows <= 16 ? append_kv8_kernel<T, D, 16> : append_kv8_kernel<T, D, 32>;
+  return launch_dependent(f, grid, dim3(ak::THREADS), smem, s, true, p.dev, Hq, Hkv, P, heads,
+                          static_cast<const T*>(q), static_cast<const T*>(k),
+                          static_cast<const T*>(v), static_cast<T*>(q_rot), k_pool, v_pool, k_scale,
+                          v_scale, frozen, status);
 }
 
 cudaError_t launch_append_kv8(const pie_fwd_plan_t& p, const void* q, const void* k, const void* v,

@@ -204,12 +204,10 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
 
   if (warp == WARPS) {
     // ---------------- producer warp -----------------------------------------
-    // Lane 2i + c copies the K (c = 0) or V (1) block of the stage's page i and
-    // leaves its scale's exponent beside the stage; page ids are fetched two
-    // stages ahead and scales one, so that neither load is waited for.
+    // Lane 2i + c copies the K (c = 0) or V (1) block of the stage's page i and,
+    // while they are on their way, leaves its scale's exponent beside the stage.
     const uint64_t pol = policy_evict_first();
-    const int c = lane & 1, pi = lane >> 1;
-    const uint8_t* scale = c ? v_scale : k_scale;
+    const int c = lane & 1, pi = lane >> 1, lp = fp8::log2i(P), ppt = kStageSlots >> lp;
     int gs = 0;  // stages issued by this CTA so far
     // every way out counts the CTA done; the last one sets the counter back
     auto finish = [&]() {
@@ -238,55 +236,47 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
       }
       if (idx < 0) break;
       const DecItem it = items[idx];
-      const int32_t* pages = m.page_ids + m.page_indptr[it.lane];
-      const int skip = window_pages(it.block);
-      Stages st_it(m, mask_words, it);
-      // this lane's page of stage s (-1: none)
-      auto page_of = [&](int s) -> int {
-        if (s >= st_it.n) return -1;
-        const int sb = it.kv_begin + s * kStageSlots;
-        const int pg = sb / P + pi;
-        if (pi >= MAX_PAGES || pg > (min(sb + kStageSlots, it.kv_end) - 1) / P) return -1;
-        return pages[pg + (pg >= m.sink_pages ? skip : 0)];
-      };
-      auto exp_of = [&](int pid) -> int {
-        return pid >= 0 && pid < m.num_pool_pages ? int(scale[int64_t(pid) * Hkv + it.kv_head]) - fp8::kBias
-                                                  : 0;
-      };
-      int s = st_it.from(0);
-      int s1 = s < st_it.n ? st_it.from(s + 1) : s;
-      int pid = page_of(s), pid1 = page_of(s1);
-      int ex = exp_of(pid);
-      for (int ord = 0; s < st_it.n; ++ord, ++gs) {
-        if (ord == m.test_stall - 1) {  // test hook: no copy of this or any later stage
-          finish();
-          return;
-        }
+      Stages seen(m, mask_words, it);
+      auto issue_stage = [&](int ord, int s, int pid, int ek, int ev) -> bool {
+        if (ord == m.test_stall - 1) return false;  // test hook: nothing from here on
         const int st = gs % STAGES, use = gs / STAGES;
         if (use > 0 && !mbar_wait_ns(&empty[st], (use - 1) & 1, wait_ns)) {
           if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
-          finish();
-          return;
+          return false;
         }
-        const int sb = it.kv_begin + s * kStageSlots;
-        const int np = (min(sb + kStageSlots, it.kv_end) - 1) / P - sb / P + 1;
-        const bool issue = pid >= 0 && pid < m.num_pool_pages;
+        const bool issue = pi < ppt && pid >= 0;
         const uint32_t copies = __popc(__ballot_sync(0xffffffffu, issue));
-        if (pi < MAX_PAGES) exps[(st * 2 + c) * MAX_PAGES + pi] = ex;
-        __syncwarp();
         if (lane == 0) {
-          if (copies != 2u * uint32_t(np)) set_status(status, PIE_STATUS_BOUNDS);
-          mbar_arrive_expect_tx(&full[st], copies * uint32_t(P) * D);
+          const int sb = it.kv_begin + s * kStageSlots;
+          if (copies != 2u * uint32_t(((min(sb + kStageSlots, it.kv_end) - 1) >> lp) - (sb >> lp) + 1))
+            set_status(status, PIE_STATUS_BOUNDS);
+          mbar_expect_tx(&full[st], copies * uint32_t(P) * D);
         }
         __syncwarp();
         if (issue)
           tma_3d(ring + st * C::STAGE + c * C::HALF + pi * P * D, c ? &vmap : &kmap,
                  int(int64_t(pid) * Hkv + it.kv_head), &full[st], pol);
-        s = s1;
-        pid = pid1;
-        ex = exp_of(pid);
-        s1 = s < st_it.n ? st_it.from(s + 1) : s;
-        pid1 = page_of(s1);
+        if (pi < MAX_PAGES) exps[(st * 2 + c) * MAX_PAGES + pi] = (c ? ev : ek) - fp8::kBias;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        ++gs;
+        return true;
+      };
+      const int i = pi < ppt ? pi : 0;
+      auto stage_at = [&](int j) { return it.kv_begin + j * kStageSlots; };
+      fp8::PageBatches pb(m, it.lane, window_pages(it.block), it.kv_head, it.kv_end, seen.n, Hkv, P,
+                          k_scale, v_scale, stage_at);
+      int next = seen.from(0);
+      for (int s = 0, ord = 0; s < seen.n; ++s) {
+        pb.at(s);
+        if (s != next) continue;
+        const int pid = pb.page(s, i), ek = pb.k_exp(s, i), ev = pb.v_exp(s, i);
+        if (!issue_stage(ord, s, pid, ek, ev)) {
+          finish();
+          return;
+        }
+        ++ord;
+        next = seen.from(s + 1);
       }
     }
     finish();
@@ -299,7 +289,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
   const int g = lane >> 2, t = lane & 3;
   const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: lane i serves row i & 7 of matrix i >> 3
   const uint32_t ring_s = smem_u32(ring);
-  const int unit = warp * kWarpSlots;
+  const int unit = warp * kWarpSlots, lp = fp8::log2i(P);
   int gs = 0;
   bool dead = false;  // a wait ran out: no more work, but every barrier is still taken
   for (int k = 0;; ++k) {
@@ -465,7 +455,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
         float lv[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int pg = (unit + g + 8 * j) / P;
+          const int pg = (unit + g + 8 * j) >> lp;
           const int ek = exps[st * 2 * MAX_PAGES + pg], ev = exps[(st * 2 + 1) * MAX_PAGES + pg];
           sk[j] = fp8::pow2i(ek);
           unsv[j] = fp8::pow2i(-ev);

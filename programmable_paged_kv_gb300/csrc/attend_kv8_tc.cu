@@ -202,47 +202,37 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
 
   if (warp == 0) {
     // ---------------- producer -----------------------------------------------
-    // lane 2i + c: the K (c = 0) or V (1) codes of the tile's page i, and the
-    // exponent of its scale; page ids two tiles ahead, exponents one
+    // lane 2i + c: the K (c = 0) or V (1) codes of the tile's page i, and, while
+    // they are on their way, the exponent of its scale
     const uint64_t pol = policy_evict_first();
     const int c = lane & 1, pi = lane >> 1;
-    const uint8_t* scale = c ? v_scale : k_scale;
-    const int32_t* pages = m.page_ids + m.page_indptr[it.lane];
-    auto page_of = [&](int j) -> int {
-      if (j >= T || pi >= MAX_PAGES) return -1;
-      const int ts = tile_at(j), pg = ts / P + pi;
-      if (pg > (min(ts + BN, ke) - 1) / P) return -1;
-      return pages[pg + (pg >= m.sink_pages ? it.skip : 0)];
-    };
-    auto exp_of = [&](int pid) -> int {
-      return pid >= 0 && pid < m.num_pool_pages
-                 ? int(scale[int64_t(pid) * Hkv + it.kv_head]) - fp8::kBias : 0;
-    };
-    int pid = page_of(0), pid1 = page_of(1);
-    int ex = exp_of(pid);
+    const int lp = fp8::log2i(P), ppt = BN >> lp;
+    fp8::PageBatches pb(m, it.lane, it.skip, it.kv_head, ke, T, Hkv, P, k_scale, v_scale, tile_at);
     for (int j = 0; j < T; ++j) {
       const int st = j % RS;
       if (j >= RS && !mbar_wait(&S.raw_empty[st], ((j / RS) - 1) & 1)) {
         bad = true;
         break;
       }
-      const bool issue = pid >= 0 && pid < m.num_pool_pages;
+      pb.at(j);
+      const int i = pi < ppt ? pi : 0;
+      const int pid = pb.page(j, i);
+      const bool issue = pi < ppt && pid >= 0;
       const uint32_t copies = __popc(__ballot_sync(0xffffffffu, issue));
-      if (pi < MAX_PAGES) S.exps[st][c][pi] = ex;
-      __syncwarp();
       if (lane == 0) {
         const int ts = tile_at(j);
-        if (copies != 2u * uint32_t((min(ts + BN, ke) - 1) / P - ts / P + 1))
+        if (copies != 2u * uint32_t(((min(ts + BN, ke) - 1) >> lp) - (ts >> lp) + 1))
           set_status(status, PIE_STATUS_BOUNDS);
-        mbar_arrive_expect_tx(&S.raw_full[st], copies * uint32_t(P) * D);
+        mbar_expect_tx(&S.raw_full[st], copies * uint32_t(P) * D);
       }
       __syncwarp();
       if (issue)
         tma_3d(S.raw[st] + c * BN * D + pi * P * D, c ? &vmap : &kmap,
                int(int64_t(pid) * Hkv + it.kv_head), &S.raw_full[st], pol);
-      pid = pid1;
-      ex = exp_of(pid);
-      pid1 = page_of(j + 2);
+      const int ek = pb.k_exp(j, i), ev = pb.v_exp(j, i);
+      if (pi < MAX_PAGES) S.exps[st][c][pi] = (c ? ev : ek) - fp8::kBias;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.raw_full[st]);
     }
   } else if (warp < C::kConv0) {
     // ---------------- MMA issuers ----------------------------------------------
@@ -300,6 +290,7 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
     // threads of a row's store hit 8 distinct banks.
     const int ct = threadIdx.x - 32 * C::kConv0;
     constexpr int RSTEP = 4 * C::CONVERTERS;
+    const int lp = fp8::log2i(P);
     const int c = ct & 7, r0 = ct >> 3, h = c >> 2;
     for (int j = 0; j < T; ++j) {
       const int rs = j % RS, st = j % NS;
@@ -310,7 +301,7 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
       }
       const int valid = min(BN, ke - tile_at(j));
       if (ct < BN / 8) {
-        const int pg = 8 * ct / P;
+        const int pg = (8 * ct) >> lp;
         const int ev = S.exps[rs][1][pg];
         S.sc[st][ct] = make_float4(fp8::pow2i(S.exps[rs][0][pg]), float(ev), fp8::pow2i(-ev), 0.f);
       }

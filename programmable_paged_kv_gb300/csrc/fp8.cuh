@@ -45,5 +45,74 @@ __device__ __forceinline__ int query_exp(float big) {
   return min(100, 13 - (int(__float_as_uint(big) >> 23) - 127));
 }
 
+__device__ __forceinline__ int log2i(int x) { return __ffs(x) - 1; }
+
+// A producer warp's look at the pages of an item's 64-slot tiles: 32 pages (64 /
+// P per tile) a batch, one per lane, with the exponents of their scales.  Page
+// ids are loaded two batches ahead and exponents one, so that a page's scale --
+// a byte of its own sector in a large pool -- is on its way for P / 2 tiles
+// before the tile needs it.
+template <typename TileAt>
+struct PageBatches {
+  const int32_t* pages;
+  const uint8_t *k_scale, *v_scale;
+  int Hkv, kv_head, lp, ke, sink_pages, skip, num_pool_pages, tiles, lppt, ltpb, lane;  // l..: log2
+  TileAt tile_at;  // first position of tile j
+  int pid, ek, ev, pid1, ek1, ev1, pid2;
+
+  __device__ __forceinline__ int page_of(int batch) const {
+    const int j = (batch << ltpb) + (lane >> lppt);
+    if (j >= tiles) return -1;
+    const int ts = tile_at(j), pg = (ts >> lp) + (lane & ((1 << lppt) - 1));
+    if (pg > (min(ts + kStageSlots, ke) - 1) >> lp) return -1;
+    const int id = pages[pg + (pg >= sink_pages ? skip : 0)];
+    return id >= 0 && id < num_pool_pages ? id : -1;
+  }
+  __device__ __forceinline__ void exps_of(int id, int& k, int& v) const {
+    k = v = kBias;
+    if (id >= 0) {
+      const int64_t at = int64_t(id) * Hkv + kv_head;
+      k = k_scale[at];
+      v = v_scale[at];
+    }
+  }
+  __device__ __forceinline__ PageBatches(const DevMeta& m, int lane_of, int skip_, int kv_head_,
+                                         int ke_, int tiles_, int Hkv_, int P_, const uint8_t* ks,
+                                         const uint8_t* vs, TileAt at)
+      : pages(m.page_ids + m.page_indptr[lane_of]), k_scale(ks), v_scale(vs), Hkv(Hkv_),
+        kv_head(kv_head_), lp(log2i(P_)), ke(ke_), sink_pages(m.sink_pages), skip(skip_),
+        num_pool_pages(m.num_pool_pages), tiles(tiles_), lppt(6 - lp), ltpb(lp - 1),
+        lane(threadIdx.x & 31), tile_at(at) {
+    static_assert(kStageSlots == 64, "tiles of 64 slots");
+    pid = page_of(0);
+    pid1 = page_of(1);
+    pid2 = page_of(2);
+    exps_of(pid, ek, ev);
+    exps_of(pid1, ek1, ev1);
+  }
+  // before tile j, in order: move to the batch that holds it
+  __device__ __forceinline__ void at(int j) {
+    if (j > 0 && (j & ((1 << ltpb) - 1)) == 0) {
+      pid = pid1, ek = ek1, ev = ev1;
+      pid1 = pid2;
+      exps_of(pid1, ek1, ev1);
+      pid2 = page_of((j >> ltpb) + 2);
+    }
+  }
+  __device__ __forceinline__ int from(int j, int i) const {
+    return ((j & ((1 << ltpb) - 1)) << lppt) + i;
+  }
+  // page i of tile j (-1: none, or outside the pool), and its scales' bytes
+  __device__ __forceinline__ int page(int j, int i) const {
+    return __shfl_sync(0xffffffffu, pid, from(j, i));
+  }
+  __device__ __forceinline__ int k_exp(int j, int i) const {
+    return __shfl_sync(0xffffffffu, ek, from(j, i));
+  }
+  __device__ __forceinline__ int v_exp(int j, int i) const {
+    return __shfl_sync(0xffffffffu, ev, from(j, i));
+  }
+};
+
 }  // namespace fp8
 }  // namespace pie

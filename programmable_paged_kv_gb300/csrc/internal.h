@@ -217,6 +217,7 @@ struct pie_fwd_plan {
   int32_t num_comb_merge;    // combine entries with chunks to merge (0: no combine launch)
   bool kv8;                  // the pools hold 8-bit codes (pie_fwd_cache.kv_type)
   int32_t num_wblocks, num_wide_items;
+  int32_t max_wrows;         // most rows that write one page
   const uint32_t* mask_set;  // mask words whose compacted lists the workspace holds
                              // (pie_fwd_set_mask), or NULL
   pie::DevMeta dev;

@@ -786,6 +786,7 @@ int pie_fwd_cache_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   p->kv8 = H.kv8;
   p->num_wblocks = static_cast<int32_t>(H.wblocks.size());
   p->num_wide_items = static_cast<int32_t>(H.wide.size());
+  for (const WriteBlock& b : H.wblocks) p->max_wrows = std::max(p->max_wrows, b.nrows);
   char* w = static_cast<char*>(dev_workspace);
   DevMeta& dm = p->dev;
   dm.row_indptr = reinterpret_cast<const int32_t*>(w + Y.row_indptr);
