@@ -163,17 +163,19 @@ def copy_pages(pools, src, dst, status=None, stream=None) -> None:
     line = torch.Size((n_pairs,))
     src_p, dst_p = p(src, "src", line, torch.int32), p(dst, "dst", line, torch.int32)
     status_p = p(status, "status", None, 4)
-    ptrs, sizes, pages = [], [], None
+    ptrs, sizes, pages, here = [], [], -1, p.device
     for t in pools:
-        n = t.shape[0] if t.dim() else -1
-        if pages is None:
+        if t.dim() == 0 or not t.is_contiguous() or t.get_device() != here:
+            raise ValueError("a pool must be a contiguous tensor of pages on the current CUDA device")
+        n = t.size(0)
+        if n != pages:
+            if pages >= 0:
+                raise ValueError("the pools must have the same number of pages")
             pages = n
-        if n != pages or n < 0:
-            raise ValueError("the pools must have the same number of pages")
-        ptr = p(t, "pool")
-        if t.nbytes:  # (a pool whose pages hold nothing has nothing to copy)
-            ptrs.append(ptr)
-            sizes.append(t.nbytes // n)
+        size = t.nbytes
+        if size:  # (a pool whose pages hold nothing has nothing to copy)
+            ptrs.append(t.data_ptr())
+            sizes.append(size // n)
     if not ptrs or n_pairs == 0:
         return
     ptrs, sizes = np.array(ptrs, np.uint64), np.array(sizes, np.int64)

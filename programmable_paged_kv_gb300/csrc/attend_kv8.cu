@@ -29,14 +29,20 @@
 //   * a transposed V fragment holds two neighbouring elements of d for two
 //     slots; one byte permutation makes them two pairs of slots, and the rows of
 //     O^T come out in the order 0, 2, .. 14, 1, 3, .. 15 of each 16.
-// One CTA (4 compute warps of 16 slots each of a 64-slot stage, one producer
-// warp) streams an item's chunk through a ring of tensor copies with a swizzle
-// that keeps ldmatrix free of bank conflicts; a persistent grid takes items from
-// a counter.  Items hold up to 8 query vectors (NT = 1: decode rows, bound by
+// One CTA (4 compute warps and a producer warp) streams an item's chunk through a
+// ring of 64-slot stages, filled by tensor copies with a swizzle that keeps
+// ldmatrix free of bank conflicts.  Two warps share a stage, 32 slots each, and
+// the pairs take turns: at 2 d bytes per slot it is the issue slots that run
+// short, and two 16-slot units side by side share one softmax step's shuffles and
+// tests.  Units that every query vector sees in full skip the tests.  A persistent
+// grid takes items from a counter.  Items hold up to 8 query vectors (NT = 1: decode rows, bound by
 // HBM: a slot and kv head costs 2 d bytes) or 32 (NT = 4: drafts and prompts
 // that attend_kv8_tc.cu does not take, every code converted once for all of them).
 // Masked passes skip stages that no row of the item sees.  Every wait is
 // bounded in time.
+
+#include <cfloat>
+#include <climits>
 
 #include <algorithm>
 
@@ -59,13 +65,17 @@ struct Cfg {
   static constexpr int STAGE = 2 * HALF;
   // 48 KB of ring per CTA at d 128: three CTAs per SM keep 144 KB in flight
   static constexpr int STAGES = D == 128 ? 3 : 6;
+  // barriers of the stages: an even number, at least the ring's, so that each
+  // belongs to one pair of warps, which then sees every phase of it
+  static constexpr int BARS = (STAGES + 1) / 2 * 2;
   static constexpr int QROW = D * 2 + 32;                // fp16 query vector, padded by 32 bytes:
                                                          // 8 rows' 8-byte reads cover all banks
   static constexpr int Q = 8 * NT * QROW * (SPLIT ? 2 : 1);
-  static constexpr int MERGE = WARPS * 8 * (D + 2) * 4;  // the warps' states of one query tile
+  static constexpr int OROW = D + 4;                     // (float2 stores of 4 rows on distinct banks)
+  static constexpr int MERGE = WARPS * 8 * (OROW + 2) * 4;  // the warps' states of one query tile
   static constexpr int SCALES = STAGES * 2 * MAX_PAGES * 4;
   static constexpr int SMEM = STAGES * STAGE + Q + MERGE + SCALES + 8 * NT * 4 +
-                              (2 * STAGES + 4) * 8 + 32 + 1024;
+                              (2 * BARS + 4) * 8 + 32 + 1024;
   static constexpr int MIN_CTAS = NT == 1 ? 3 : 1;
 };
 
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
   using namespace a8;
   constexpr bool SPLIT = sizeof(T) == 4;
   using C = Cfg<D, NT, SPLIT>;
-  constexpr int STAGES = C::STAGES, KS = C::KS;
+  constexpr int STAGES = C::STAGES, BARS = C::BARS, KS = C::KS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -180,16 +190,16 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
   int* exps = reinterpret_cast<int*>(merge + C::MERGE / 4);      // [STAGES][K, V][pages] exponents
   float* zq = reinterpret_cast<float*>(exps + C::SCALES / 4);    // [8 NT] score factors
   uint64_t* full = reinterpret_cast<uint64_t*>(zq + 8 * NT);
-  uint64_t* empty = full + STAGES;
-  uint64_t* item_full = empty + STAGES;
+  uint64_t* empty = full + BARS;
+  uint64_t* item_full = empty + BARS;
   uint64_t* item_empty = item_full + 2;
   int* qidx = reinterpret_cast<int*>(item_empty + 2);
   int* decision = qidx + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < BARS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], WARPS);
+      mbar_init(&empty[s], WARPS / 2);  // the pair of warps that reads it
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&item_full[q], 1);
@@ -219,10 +229,10 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
         }
       }
     };
+    int ticket = 0;  // lane 0: the next item, asked for while the last one streams
+    if (lane == 0) ticket = atomicAdd(work, 1);
     for (int k = 0;; ++k) {
-      int idx = 0;
-      if (lane == 0) idx = atomicAdd(work, 1);
-      idx = __shfl_sync(0xffffffffu, idx, 0);
+      int idx = __shfl_sync(0xffffffffu, ticket, 0);
       if (idx >= num_items) idx = -1;
       const int q = k & 1;
       if (k >= 2 && !mbar_wait_ns(&item_empty[q], ((k >> 1) - 1) & 1, wait_ns)) {
@@ -235,12 +245,15 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
         mbar_arrive(&item_full[q]);
       }
       if (idx < 0) break;
+      if (lane == 0) ticket = atomicAdd(work, 1);
       const DecItem it = items[idx];
       Stages seen(m, mask_words, it);
       auto issue_stage = [&](int ord, int s, int pid, int ek, int ev) -> bool {
         if (ord == m.test_stall - 1) return false;  // test hook: nothing from here on
-        const int st = gs % STAGES, use = gs / STAGES;
-        if (use > 0 && !mbar_wait_ns(&empty[st], (use - 1) & 1, wait_ns)) {
+        // the stage that held this one's place in the ring has been read
+        const int st = gs % STAGES, before = gs - STAGES;
+        uint64_t* bar = &full[gs % BARS];
+        if (before >= 0 && !mbar_wait_ns(&empty[before % BARS], (before / BARS) & 1, wait_ns)) {
           if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
           return false;
         }
@@ -250,15 +263,15 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
           const int sb = it.kv_begin + s * kStageSlots;
           if (copies != 2u * uint32_t(((min(sb + kStageSlots, it.kv_end) - 1) >> lp) - (sb >> lp) + 1))
             set_status(status, PIE_STATUS_BOUNDS);
-          mbar_expect_tx(&full[st], copies * uint32_t(P) * D);
+          mbar_expect_tx(bar, copies * uint32_t(P) * D);
         }
         __syncwarp();
         if (issue)
           tma_3d(ring + st * C::STAGE + c * C::HALF + pi * P * D, c ? &vmap : &kmap,
-                 int(int64_t(pid) * Hkv + it.kv_head), &full[st], pol);
+                 int(int64_t(pid) * Hkv + it.kv_head), bar, pol);
         if (pi < MAX_PAGES) exps[(st * 2 + c) * MAX_PAGES + pi] = (c ? ev : ek) - fp8::kBias;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
+        if (lane == 0) mbar_arrive(bar);
         ++gs;
         return true;
       };
@@ -289,7 +302,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
   const int g = lane >> 2, t = lane & 3;
   const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: lane i serves row i & 7 of matrix i >> 3
   const uint32_t ring_s = smem_u32(ring);
-  const int unit = warp * kWarpSlots, lp = fp8::log2i(P);
+  const int half = (warp & 1) * 32, pair = warp >> 1, lp = fp8::log2i(P);
   int gs = 0;
   bool dead = false;  // a wait ran out: no more work, but every barrier is still taken
   for (int k = 0;; ++k) {
@@ -353,11 +366,12 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
       }
     }
     asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-    // this lane's query vectors 8 nt + 2t + i
+    // this lane's query vectors 8 nt + 2t + i; the slots that every one sees
     bool valid_q[NT][2];
     int slot_lim[NT][2];
     float zf[NT][2];
     const uint32_t* mrow[NT][2];
+    int lim_min = INT_MAX, lim_max = -1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -366,12 +380,19 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
         valid_q[nt][i] = qv < nqv;
         const int row = it.row0 + (valid_q[nt][i] ? qv : 0) / G;
         slot_lim[nt][i] = valid_q[nt][i] ? m.slots[row] : -1;
+        if (valid_q[nt][i]) {
+          lim_min = min(lim_min, slot_lim[nt][i]);
+          lim_max = max(lim_max, slot_lim[nt][i]);
+        }
         zf[nt][i] = zq[qv];
         mrow[nt][i] = valid_q[nt][i] && mask_words ? mask_words + m.mask_word_indptr[row] : nullptr;
       }
-    // Q^T fragments: d elements 16k + 4t .. 4t + 3 of query g (one query tile
-    // keeps them in registers)
-    uint32_t qb[NT == 1 ? KS : 1][SPLIT ? 4 : 2];
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+    lim_max = __reduce_max_sync(0xffffffffu, lim_max);
+    // Q^T fragments: d elements 16k + 4t .. 4t + 3 of query g (one bf16 query
+    // tile keeps them in registers)
+    constexpr bool QREG = NT == 1 && !SPLIT;
+    uint32_t qb[QREG ? KS : 1][2];
     auto load_q = [&](int nt, int kk, uint32_t* b) {
       const uint8_t* src = qs + (nt * 8 + g) * C::QROW + kk * 32 + t * 8;
       const uint2 u = *reinterpret_cast<const uint2*>(src);
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
         b[3] = w.y;
       }
     };
-    if constexpr (NT == 1) {
+    if constexpr (QREG) {
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) load_q(0, kk, qb[kk]);
     }
@@ -398,28 +419,33 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
     }
 
     for (int s = st_it.from(0); s < st_it.n; s = st_it.from(s + 1), ++gs) {
+      if ((gs & 1) != pair || dead) continue;  // the other pair's stage
       const int st = gs % STAGES;
-      if (dead) continue;
-      const int unit_base = it.kv_begin + s * kStageSlots + unit;
-      const int nvalid = min(kWarpSlots, it.kv_end - unit_base);
-      // the rows' mask words of this unit, on their way while the stage lands
+      const int base = it.kv_begin + s * kStageSlots + half;  // this warp's first position
+      const int left = it.kv_end - base;
+      // the rows' mask words of these positions, on their way while the stage lands
       uint32_t word[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          word[nt][i] = mrow[nt][i] && nvalid > 0
-                            ? mrow[nt][i][unit_base >> 5] >> (unit_base & 31) : ~0u;
-      if (!mbar_wait_ns(&full[st], (gs / STAGES) & 1, wait_ns)) {
+        for (int i = 0; i < 2; ++i) word[nt][i] = mrow[nt][i] && left > 0 ? mrow[nt][i][base >> 5] : ~0u;
+      if (!mbar_wait_ns(&full[gs % BARS], (gs / BARS) & 1, wait_ns)) {
         dead = true;
         if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
         continue;
       }
-      if (nvalid > 0) {
+      // U units of 16 slots side by side: two, or one after the other where the
+      // query tiles take the registers
+      constexpr int U = NT == 1 ? 2 : 1;
+#pragma unroll 1
+      for (int u0 = 0; u0 < 2 && left > 16 * u0; u0 += U) {
+        const int unit = half + 16 * u0;  // first row within the stage
+        const int ub = base + 16 * u0;
+        const int nvalid = min(16 * U, left - 16 * u0);
         const uint32_t kbase = ring_s + st * C::STAGE, vbase = kbase + C::HALF;
-        if (nvalid < kWarpSlots) {
+        if (nvalid < 16 * U) {
           // V rows past the end: zero codes, so that their zero weights give zero
-          for (int i = lane; i < (kWarpSlots - nvalid) * (D / 16); i += 32)
+          for (int i = lane; i < (16 * U - nvalid) * (D / 16); i += 32)
             *reinterpret_cast<uint4*>(ring + st * C::STAGE + C::HALF +
                                       (unit + nvalid + i / (D / 16)) * D + i % (D / 16) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
@@ -428,74 +454,100 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
         }
         // ---- S^T = K Q^T: matrices (slots 0-7, chunk 2kk), (8-15, 2kk),
         // (0-7, 2kk + 1), (8-15, 2kk + 1)
-        float cc[NT][4];
+        float cc[U][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) cc[nt][0] = cc[nt][1] = cc[nt][2] = cc[nt][3] = 0.f;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            cc[u][nt][0] = cc[u][nt][1] = cc[u][nt][2] = cc[u][nt][3] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KS; kk += 2) {
-          uint32_t w[4];
-          ldsm_x4(kbase + chunk<D>(unit + (mi & 1) * 8 + mr, kk + (mi >> 1)), w);
+          uint32_t w[U][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            ldsm_x4(kbase + chunk<D>(unit + 16 * u + (mi & 1) * 8 + mr, kk + (mi >> 1)), w[u]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t a[4];
-            fp8::to_half2x2(w[2 * h], a[0], a[2]);
-            fp8::to_half2x2(w[2 * h + 1], a[1], a[3]);
+            uint32_t a[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              fp8::to_half2x2(w[u][2 * h], a[u][0], a[u][2]);
+              fp8::to_half2x2(w[u][2 * h + 1], a[u][1], a[u][3]);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               uint32_t b[SPLIT ? 4 : 2];
-              if constexpr (NT > 1) load_q(nt, kk + h, b);
-              const uint32_t* qf = NT == 1 ? qb[kk + h] : b;
-              mma(cc[nt], a, qf[0], qf[1]);
-              if constexpr (SPLIT) mma(cc[nt], a, qf[2], qf[3]);
+              if constexpr (QREG) {
+                b[0] = qb[kk + h][0];
+                b[1] = qb[kk + h][1];
+              } else {
+                load_q(nt, kk + h, b);
+              }
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                mma(cc[u][nt], a[u], b[0], b[1]);
+                if constexpr (SPLIT) mma(cc[u][nt], a[u], b[2], b[3]);
+              }
             }
           }
         }
-        // this lane's slots g and g + 8: their pages' scales
-        float sk[2], unsv[2];
-        float lv[2];
+        // this lane's slots g and g + 8 of each unit: their pages' scales
+        float sk[U][2], unsv[U][2], lv[U][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int pg = (unit + g + 8 * j) >> lp;
-          const int ek = exps[st * 2 * MAX_PAGES + pg], ev = exps[(st * 2 + 1) * MAX_PAGES + pg];
-          sk[j] = fp8::pow2i(ek);
-          unsv[j] = fp8::pow2i(-ev);
-          lv[j] = float(ev);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int pg = (unit + 16 * u + g + 8 * j) >> lp;
+            const int ek = exps[st * 2 * MAX_PAGES + pg], ev = exps[(st * 2 + 1) * MAX_PAGES + pg];
+            sk[u][j] = fp8::pow2i(ek);
+            unsv[u][j] = fp8::pow2i(-ev);
+            lv[u][j] = float(ev);
+          }
+        // positions that every query vector sees (slots rise with them)
+        const int s0 = view.slot(ub), s1 = view.slot(ub + 16 * U - 1);
+        const bool all = !mask_words && nvalid == 16 * U && s1 <= lim_min &&
+                         (view.window == 0 || s0 > lim_max - view.window || s1 < view.sinks);
+        if (!all) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = e & 1, cs = 16 * u + g + 8 * (e >> 1);
+                const bool vis = valid_q[nt][i] && cs < nvalid &&
+                                 (mrow[nt][i] ? ((word[nt][i] >> (16 * u0 + cs)) & 1u) != 0
+                                              : view.sees(slot_lim[nt][i], view.slot(ub + cs)));
+                if (!vis) cc[u][nt][e] = -INFINITY;
+              }
         }
-        uint32_t pb[NT][SPLIT ? 4 : 2];
+        uint32_t pb[U][NT][SPLIT ? 4 : 2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          // cc[e]: slot g + 8 (e >> 1), query 2t + (e & 1)
-          float zs[4];
-          float mt[2] = {-INFINITY, -INFINITY};
+          // cc[u][nt][e]: slot 16u + g + 8 (e >> 1), query 2t + (e & 1); the
+          // factors stay above zero, so that -inf stays -inf
+          float zs[U][4], mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = e >> 1, i = e & 1, cs = g + 8 * j;
-            const bool vis = valid_q[nt][i] && cs < nvalid &&
-                             (mrow[nt][i] ? ((word[nt][i] >> cs) & 1u) != 0
-                                          : view.sees(slot_lim[nt][i], view.slot(unit_base + cs)));
-            zs[e] = zf[nt][i] * sk[j];
-            cc[nt][e] = vis ? cc[nt][e] : -INFINITY;
-            if (vis) mt[i] = fmaxf(mt[i], fmaf(cc[nt][e], zs[e], lv[j]));
-          }
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              zs[u][e] = fmaxf(zf[nt][e & 1] * sk[u][e >> 1], FLT_MIN);
+              mt[e & 1] = fmaxf(mt[e & 1], fmaf(cc[u][nt][e], zs[u][e], lv[u][e >> 1]));
+            }
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
             mt[0] = fmaxf(mt[0], __shfl_xor_sync(0xffffffffu, mt[0], off));
             mt[1] = fmaxf(mt[1], __shfl_xor_sync(0xffffffffu, mt[1], off));
           }
-          float m_new[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            m_new[i] = m_used[nt][i];
-            if (mt[i] > m_used[nt][i] + 8.f || m_used[nt][i] == -INFINITY)
-              m_new[i] = fmaxf(m_used[nt][i], ceilf(mt[i]));
-          }
-          if (__any_sync(0xffffffffu, m_new[0] != m_used[nt][0] || m_new[1] != m_used[nt][1])) {
+          // (m_used + 8 is -inf at first: any visible score moves it)
+          if (__any_sync(0xffffffffu, mt[0] > m_used[nt][0] + 8.f || mt[1] > m_used[nt][1] + 8.f)) {
             float alpha[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              alpha[i] = m_new[i] == m_used[nt][i] ? 1.f : ex2(m_used[nt][i] - m_new[i]);
+              const float m_new = mt[i] > m_used[nt][i] + 8.f ? ceilf(mt[i]) : m_used[nt][i];
+              alpha[i] = m_new == m_used[nt][i] ? 1.f : ex2(m_used[nt][i] - m_new);
               l_part[nt][i] *= alpha[i];
-              m_used[nt][i] = m_new[i];
+              m_used[nt][i] = m_new;
             }
 #pragma unroll
             for (int n = 0; n < KS; ++n) {
@@ -505,53 +557,58 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
               o[nt][n][3] *= alpha[1];
             }
           }
-          float p[4];
+          // (no visible slot yet: every score is -inf, and so is every exponent)
+          const float neg_m[2] = {m_used[nt][0] == -INFINITY ? 0.f : -m_used[nt][0],
+                                  m_used[nt][1] == -INFINITY ? 0.f : -m_used[nt][1]};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float mu = m_used[nt][e & 1];
-            // (a score of -inf stays -inf whatever its scale is)
-            const float x = cc[nt][e] == -INFINITY
-                                ? -INFINITY : fmaf(cc[nt][e], zs[e], lv[e >> 1] - mu);
-            p[e] = ex2(x);
-          }
-          l_part[nt][0] += p[0] * unsv[0] + p[2] * unsv[1];
-          l_part[nt][1] += p[1] * unsv[0] + p[3] * unsv[1];
-          const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
-          pb[nt][0] = movmatrix_t(h0);
-          pb[nt][1] = movmatrix_t(h1);
-          if constexpr (SPLIT) {
-            pb[nt][2] = movmatrix_t(pack_rest(p[0], p[1], h0));
-            pb[nt][3] = movmatrix_t(pack_rest(p[2], p[3], h1));
+          for (int u = 0; u < U; ++u) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              p[e] = ex2(fmaf(cc[u][nt][e], zs[u][e], lv[u][e >> 1] + neg_m[e & 1]));
+            l_part[nt][0] = fmaf(p[0], unsv[u][0], fmaf(p[2], unsv[u][1], l_part[nt][0]));
+            l_part[nt][1] = fmaf(p[1], unsv[u][0], fmaf(p[3], unsv[u][1], l_part[nt][1]));
+            const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
+            pb[u][nt][0] = movmatrix_t(h0);
+            pb[u][nt][1] = movmatrix_t(h1);
+            if constexpr (SPLIT) {
+              pb[u][nt][2] = movmatrix_t(pack_rest(p[0], p[1], h0));
+              pb[u][nt][3] = movmatrix_t(pack_rest(p[2], p[3], h1));
+            }
           }
         }
         // ---- O^T += V^T P^T: matrices (slots 0-7, chunk n), (8-15, n), (0-7,
         // n + 1), (8-15, n + 1), transposed
 #pragma unroll
         for (int n = 0; n < KS; n += 2) {
-          uint32_t w[4];
-          ldsm_x4_t(vbase + chunk<D>(unit + (mi & 1) * 8 + mr, n + (mi >> 1)), w);
+          uint32_t w[U][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a[4];
-            fp8::to_half2x2(__byte_perm(w[2 * h], 0, 0x3120), a[0], a[1]);
-            fp8::to_half2x2(__byte_perm(w[2 * h + 1], 0, 0x3120), a[2], a[3]);
+          for (int u = 0; u < U; ++u)
+            ldsm_x4_t(vbase + chunk<D>(unit + 16 * u + (mi & 1) * 8 + mr, n + (mi >> 1)), w[u]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(o[nt][n + h], a, pb[nt][0], pb[nt][1]);
-              if constexpr (SPLIT) mma(o[nt][n + h], a, pb[nt][2], pb[nt][3]);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              uint32_t a[4];
+              fp8::to_half2x2(__byte_perm(w[u][2 * h], 0, 0x3120), a[0], a[1]);
+              fp8::to_half2x2(__byte_perm(w[u][2 * h + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma(o[nt][n + h], a, pb[u][nt][0], pb[u][nt][1]);
+                if constexpr (SPLIT) mma(o[nt][n + h], a, pb[u][nt][2], pb[u][nt][3]);
+              }
             }
-          }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (lane == 0) mbar_arrive(&empty[gs % BARS]);
     }
 
     // ---- merge the warps' states into the item's partials, a query tile at a
     // time (the buffer's last readers have passed the barriers since)
     float* mw = merge;            // [WARPS][8]
     float* lw = mw + WARPS * 8;   // [WARPS][8]
-    float* ow = lw + WARPS * 8;   // [WARPS][8][D]
+    float* ow = lw + WARPS * 8;   // [WARPS][8][OROW]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (nt * 8 >= nqv) break;
@@ -566,7 +623,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
           mw[warp * 8 + q] = m_used[nt][i];
           lw[warp * 8 + q] = l;
         }
-        float* orow = ow + (warp * 8 + q) * D;
+        float* orow = ow + (warp * 8 + q) * C::OROW;
 #pragma unroll
         for (int n = 0; n < KS; ++n)
           *reinterpret_cast<float2*>(orow + 16 * n + 2 * g) = make_float2(o[nt][n][i], o[nt][n][2 + i]);
@@ -583,7 +640,7 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
           for (int w = 0; w < WARPS; ++w) {
             const float mv = mw[w * 8 + qq];
             const float f = mv == -INFINITY ? 0.f : ex2(mv - M);
-            O = fmaf(f, ow[(w * 8 + qq) * D + cd], O);
+            O = fmaf(f, ow[(w * 8 + qq) * C::OROW + cd], O);
             L = fmaf(f, lw[w * 8 + qq], L);
           }
         }

@@ -24,6 +24,9 @@
 // NT = 2, and runs beside it.  Masked passes walk only the tiles some row of the
 // item sees, listed once at the start.  Every wait is bounded in time.
 
+#include <cfloat>
+#include <climits>
+
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -414,15 +417,15 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
             s[c] = vis ? s[c] : -INFINITY;
           }
         }
-        // the largest x = zf 2^ek s + ev (zf > 0: the maximum of 8 slots of one
-        // page commutes with it)
+        // the largest x = zf 2^ek s + ev (the factor stays above zero: the maximum of
+        // 8 slots of one page commutes with it, and -inf stays -inf)
         float mx = -INFINITY;
 #pragma unroll
         for (int g8 = 0; g8 < BN / 8; ++g8) {
           const float2 sc = *reinterpret_cast<const float2*>(&S.sc[st][g8]);
           const float* e = s + 8 * g8;
           const float m8 = max3(max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), fmaxf(e[6], e[7]));
-          mx = fmaxf(mx, fmaf(m8, zf * sc.x, sc.y));
+          mx = fmaxf(mx, fmaf(m8, fmaxf(zf * sc.x, FLT_MIN), sc.y));
         }
         float m_new = m_used;
         if (m_used == -INFINITY || mx > m_used + 8.f) m_new = fmaxf(m_used, ceilf(mx));
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
 #pragma unroll
         for (int g8 = 0; g8 < BN / 8; ++g8) {
           const float4 sc = S.sc[st][g8];
-          const float a = zf * sc.x, b = sc.y + neg_m;
+          const float a = fmaxf(zf * sc.x, FLT_MIN), b = sc.y + neg_m;
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
