@@ -9,15 +9,20 @@
 //
 // One CTA takes a work item: NT (1 or 2) tiles of 128 query vectors against a
 // chunk of the lane's slots, in tiles of BN = 64 slots.
-//   warp 0       producer: the codes of a tile's pages, one tensor copy per page
-//                and tensor, into a ring of raw stages;
-//   warps 1..NT  one MMA issuer per query tile: S = Q K^T (128 x 64) into one of
-//                two TMEM score buffers, O += P V (128 x 128) with P in TMEM;
-//   2 or 4 warps converters: raw codes (16 per thread and step) to fp16 in the
-//                128-byte-swizzled operand layout, rows past the end as zeros;
-//                one conversion serves all query tiles;
-//   4 NT warps   softmax: a thread per query row (its TMEM lane), which first
-//                writes its own scaled query vector into the operand tile.
+//   warp 0        producer: the codes of a tile's pages, one tensor copy per page
+//                 and tensor, into a ring of raw stages;
+//   warps 1..NT   one MMA issuer per query tile: S = Q K^T (128 x 64) into one of
+//                 two TMEM score buffers, O += P V (128 x 128) with P in TMEM.  The
+//                 whole warp walks the loop and one elected lane issues, so that
+//                 the descriptors stay in uniform registers (a branch on the lane
+//                 cost about 100 cycles per MMA);
+//   warps 4..7    converters, two for K and two for V: raw codes (16 per thread
+//                 and step) to fp16 in the 128-byte-swizzled operand layout, rows
+//                 past the end as zeros; one conversion serves all query tiles;
+//   warps 8..     softmax, 4 per query tile: a thread per query row (its TMEM
+//                 lane); first they write the scaled query vectors into the operand
+//                 tile.  With two query tiles they take registers over
+//                 from the other warps (128 each at launch; 168 and 88).
 // Scores of tile j + 2 are issued behind P.V of tile j, so a softmax step never
 // waits for them.  The conversion costs 1 shared load, 8 conversions and 2
 // shared stores per 16 codes, about a third of the softmax's issue slots with
@@ -49,10 +54,7 @@ template <int NT>
 struct Cfg {
   static constexpr int RS = NT == 1 ? 5 : 3;  // raw stages
   static constexpr int NS = 3;                // operand stages
-  static constexpr int CONVERTERS = NT == 1 ? 4 : 2;  // warps (two leave the softmax its registers)
-  static constexpr int kIssuer0 = 1;
-  static constexpr int kConv0 = 1 + NT;
-  static constexpr int kSoft0 = kConv0 + CONVERTERS;
+  static constexpr int kIssuer0 = 1, kConv0 = 4, kSoft0 = 8;
   static constexpr int kThreads = 32 * kSoft0 + 128 * NT;
   static constexpr uint32_t kTmemCols = NT == 1 ? 256 : 512;
 };
@@ -115,6 +117,39 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int z,
       : "memory");
 }
 
+// tc::mma_ss, tc::mma_ts and tc::commit by one elected lane of a whole warp
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+// mbar_wait of a whole warp, with one answer
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// bits [0, n) of a word
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
 }  // namespace t8
 
 template <int NT>
@@ -130,7 +165,7 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
   Smem<NT>& S = *reinterpret_cast<Smem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const TcItem it = m.tc_items[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int kb = it.kv_begin, ke = it.kv_end;
   const int nqv = it.nrows * G;
   const int all_tiles = ke > kb ? (ke - kb + BN - 1) / BN : 0;
@@ -140,11 +175,11 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
     mbar_init(&S.q_full, 4 * NT);
     for (int i = 0; i < RS; ++i) {
       mbar_init(&S.raw_full[i], 1);
-      mbar_init(&S.raw_empty[i], C::CONVERTERS);
+      mbar_init(&S.raw_empty[i], 4);
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&S.k_full[i], C::CONVERTERS);
-      mbar_init(&S.v_full[i], C::CONVERTERS);
+      mbar_init(&S.k_full[i], 2);
+      mbar_init(&S.v_full[i], 2);
       mbar_init(&S.kv_empty[i], NT);
     }
     for (int t = 0; t < NT; ++t) {
@@ -200,6 +235,11 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
   tc::fence_after();
   const uint32_t tmem = S.tmem_base;
   bool bad = false;
+  if constexpr (NT == 2) {
+    // 256 threads at 88 and 256 at 168 registers: the 65,536 of the launch
+    if (warp < C::kSoft0) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+  }
   // first slot position of the item's j-th tile
   auto tile_at = [&](int j) { return kb + (mask_words ? int(S.tiles[j]) : j) * BN; };
 
@@ -239,41 +279,43 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
     }
   } else if (warp < C::kConv0) {
     // ---------------- MMA issuers ----------------------------------------------
-    if (lane == 0 && T > 0) {
+    if (warp < C::kIssuer0 + NT && T > 0) {
       const int t = warp - C::kIssuer0;
       constexpr uint32_t ID_S = idesc16(128, BN, false);
       constexpr uint32_t ID_O = idesc16(128, 128, true);
       const uint64_t dq = tc::sdesc(S.q[t][0], 16, 1024);
       const uint64_t dk = tc::sdesc(S.k[0][0], 16, 1024);
       const uint64_t dv = tc::sdesc(S.v[0][0], HALF, 1024);
-      const uint32_t tO = tmem + o_col<NT>(t);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t tO = tm + o_col<NT>(t);
       auto issue_s = [&](int j) -> bool {
         const int st = j % NS;
-        if (!mbar_wait(&S.k_full[st], (j / NS) & 1)) return false;
+        if (!warp_wait(&S.k_full[st], (j / NS) & 1)) return false;
         tc::fence_after();
         const uint64_t bk = dk + uint64_t(st) * (2 * HALF >> 4);
+        const uint32_t d = tm + s_col<NT>(t, j & 1);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc::mma_ss(tmem + s_col<NT>(t, j & 1), dq + uint64_t((k >> 2) * (128 * 128 >> 4) + (k & 3) * 2),
-                     bk + uint64_t((k >> 2) * (HALF >> 4) + (k & 3) * 2), ID_S, k > 0 ? 1u : 0u);
-        tc::commit(&S.s_full[t][j & 1]);
+          mma_ss(d, dq + uint64_t((k >> 2) * (128 * 128 >> 4) + (k & 3) * 2),
+                 bk + uint64_t((k >> 2) * (HALF >> 4) + (k & 3) * 2), ID_S, k > 0 ? 1u : 0u);
+        commit(&S.s_full[t][j & 1]);
         return true;
       };
       auto issue_pv = [&](int j) -> bool {
-        if (!mbar_wait(&S.p_full[t][j & 1], (j >> 1) & 1)) return false;
+        if (!warp_wait(&S.p_full[t][j & 1], (j >> 1) & 1)) return false;
         const int st = j % NS;
-        if (!mbar_wait(&S.v_full[st], (j / NS) & 1)) return false;
+        if (!warp_wait(&S.v_full[st], (j / NS) & 1)) return false;
         tc::fence_after();
         const int ksteps = (min(BN, ke - tile_at(j)) + 15) >> 4;
         const uint64_t bv = dv + uint64_t(st) * (2 * HALF >> 4);
-        const uint32_t ta = tmem + s_col<NT>(t, j & 1);
+        const uint32_t ta = tm + s_col<NT>(t, j & 1);
         for (int k = 0; k < ksteps; ++k)
-          tc::mma_ts(tO, ta + 8 * k, bv + uint64_t(k) * (2048 >> 4), ID_O, (j > 0 || k > 0) ? 1u : 0u);
-        tc::commit(&S.o_done[t][j & 1]);
-        tc::commit(&S.kv_empty[st]);
+          mma_ts(tO, ta + 8 * k, bv + uint64_t(k) * (2048 >> 4), ID_O, (j > 0 || k > 0) ? 1u : 0u);
+        commit(&S.o_done[t][j & 1]);
+        commit(&S.kv_empty[st]);
         return true;
       };
-      bool ok = mbar_wait(&S.q_full, 0);
+      bool ok = warp_wait(&S.q_full, 0);
       tc::fence_after();
       for (int j = 0; j < 2 && j < T && ok; ++j) ok = issue_s(j);
       for (int j = 0; j < T && ok; ++j) {
@@ -281,60 +323,67 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
         if (ok && j + 2 < T) ok = issue_s(j + 2);
       }
       // every MMA of this issuer has finished before TMEM is released
-      tc::commit(&S.mma_done[t]);
-      if (!mbar_wait(&S.mma_done[t], 0)) ok = false;
+      commit(&S.mma_done[t]);
+      if (!warp_wait(&S.mma_done[t], 0)) ok = false;
       bad = !ok;
     }
   } else if (warp < C::kSoft0) {
     // ---------------- converters -------------------------------------------------
-    // thread: 16-byte chunk c of rows r0, r0 + RSTEP, ..; its 16 codes become two
-    // 16-byte chunks of the operand row (half c / 4 of d).  The upper half's
-    // threads write their two chunks in the other order, so that the 8
-    // threads of a row's store hit 8 distinct banks.
-    const int ct = threadIdx.x - 32 * C::kConv0;
-    constexpr int RSTEP = 4 * C::CONVERTERS;
-    const int lp = fp8::log2i(P);
+    // Warps 4, 5 take K, 6 and 7 V.  Thread: 16-byte chunk c of rows r0, r0 + 8,
+    // ..; its 16 codes become two 16-byte chunks of the operand row (half c / 4
+    // of d).  The upper half's threads write their two chunks in the other order,
+    // so that the 8 threads of a row's store hit 8 distinct banks.  The raw stage
+    // is released as soon as its codes are in registers.
+    const int kv = (warp - C::kConv0) >> 1;
+    const int ct = (threadIdx.x - 32 * C::kConv0) & 63;
     const int c = ct & 7, r0 = ct >> 3, h = c >> 2;
+    const int lp = fp8::log2i(P);
+    uint64_t* done = kv ? S.v_full : S.k_full;
     for (int j = 0; j < T; ++j) {
       const int rs = j % RS, st = j % NS;
-      if (!mbar_wait(&S.raw_full[rs], (j / RS) & 1) ||
-          (j >= NS && !mbar_wait(&S.kv_empty[st], ((j / NS) - 1) & 1))) {
+      if (!mbar_wait(&S.raw_full[rs], (j / RS) & 1)) {
         bad = true;
         break;
       }
       const int valid = min(BN, ke - tile_at(j));
-      if (ct < BN / 8) {
-        const int pg = (8 * ct) >> lp;
-        const int ev = S.exps[rs][1][pg];
-        S.sc[st][ct] = make_float4(fp8::pow2i(S.exps[rs][0][pg]), float(ev), fp8::pow2i(-ev), 0.f);
-      }
+      const uint8_t* src = S.raw[rs] + kv * BN * D;
+      uint4 u[BN / 8];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t* src = S.raw[rs] + kv * BN * D;
-        uint8_t* dst = kv ? S.v[st][h] : S.k[st][h];
-#pragma unroll
-        for (int i = 0; i < BN / RSTEP; ++i) {
-          const int r = r0 + RSTEP * i;
-          uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (r < valid) u = *reinterpret_cast<const uint4*>(src + r * D + c * 16);
-          uint32_t f[8];
-          fp8::to_half2x2(u.x, f[0], f[1]);
-          fp8::to_half2x2(u.y, f[2], f[3]);
-          fp8::to_half2x2(u.z, f[4], f[5]);
-          fp8::to_half2x2(u.w, f[6], f[7]);
-          const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), b = make_uint4(f[4], f[5], f[6], f[7]);
-          const int dc = 2 * (c & 3);
-          uint8_t* row = dst + r * 128;
-          *reinterpret_cast<uint4*>(row + (((dc + h) ^ (r & 7)) << 4)) = h ? b : a;
-          *reinterpret_cast<uint4*>(row + (((dc + 1 - h) ^ (r & 7)) << 4)) = h ? a : b;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(kv ? &S.v_full[st] : &S.k_full[st]);
-          if (kv) mbar_arrive(&S.raw_empty[rs]);
-        }
+      for (int i = 0; i < BN / 8; ++i) {
+        const int r = r0 + 8 * i;
+        u[i] = r < valid ? *reinterpret_cast<const uint4*>(src + r * D + c * 16)
+                         : make_uint4(0u, 0u, 0u, 0u);
       }
+      int ek = 0, ev = 0;
+      if (kv == 0 && ct < BN / 8) {
+        ek = S.exps[rs][0][(8 * ct) >> lp];
+        ev = S.exps[rs][1][(8 * ct) >> lp];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.raw_empty[rs]);
+      if (j >= NS && !mbar_wait(&S.kv_empty[st], ((j / NS) - 1) & 1)) {
+        bad = true;
+        break;
+      }
+      if (kv == 0 && ct < BN / 8)
+        S.sc[st][ct] = make_float4(fp8::pow2i(ek), float(ev), fp8::pow2i(-ev), 0.f);
+      uint8_t* dst = (kv ? S.v[st][h] : S.k[st][h]) + r0 * 128;
+      const int dc = 2 * (c & 3);
+      const int o0 = ((dc + h) ^ (r0 & 7)) << 4, o1 = ((dc + 1 - h) ^ (r0 & 7)) << 4;
+#pragma unroll
+      for (int i = 0; i < BN / 8; ++i) {
+        uint32_t f[8];
+        fp8::to_half2x2(u[i].x, f[0], f[1]);
+        fp8::to_half2x2(u[i].y, f[2], f[3]);
+        fp8::to_half2x2(u[i].z, f[4], f[5]);
+        fp8::to_half2x2(u[i].w, f[6], f[7]);
+        const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), b = make_uint4(f[4], f[5], f[6], f[7]);
+        *reinterpret_cast<uint4*>(dst + i * 1024 + o0) = h ? b : a;
+        *reinterpret_cast<uint4*>(dst + i * 1024 + o1) = h ? a : b;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&done[st]);
     }
   } else if (T > 0) {
     // ---------------- softmax groups: thread = query row ---------------------
@@ -346,37 +395,44 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
     const bool warp_live = __any_sync(0xffffffffu, valid_q);
     const int row = it.row0 + (valid_q ? q : 0) / G;
     const int head = it.kv_head * G + (valid_q ? q : 0) % G;
-    // the query vector into fp16's range, and into the operand tile
-    float zf = 0.f;
+    // the warp's 32 query vectors into fp16's range and into the operand tile, two
+    // at a time (16 lanes of 16 bytes each), their powers of two to their lanes
+    int up = 0;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(q_rot + (int64_t(row) * Hq + head) * D);
+      const int c = lane & 15;
       uint4 u[16];
-      float big = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        u[i] = valid_q ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        float x[8];
+        const int qr = t * kTcTileQueries + quad * 32 + 2 * i + (lane >> 4);
+        u[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (qr < nqv)
+          u[i] = *reinterpret_cast<const uint4*>(
+              q_rot + (int64_t(it.row0 + qr / G) * Hq + it.kv_head * G + qr % G) * D + c * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float x[8], big = 0.f;
         unpack16<__nv_bfloat16>(u[i], x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
-      }
-      const int up = fp8::query_exp(big);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x[8];
-        unpack16<__nv_bfloat16>(u[i], x);
+        for (int off = 8; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+        const int ue = fp8::query_exp(big);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fp8::scale2(x[e], up);
-        *reinterpret_cast<uint4*>(S.q[t][i >> 3] + qm * 128 + (((i & 7) ^ (qm & 7)) << 4)) =
+        for (int e = 0; e < 8; ++e) x[e] = fp8::scale2(x[e], ue);
+        const int r = quad * 32 + 2 * i + (lane >> 4);
+        *reinterpret_cast<uint4*>(S.q[t][c >> 3] + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
             make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]),
                        pack_half(x[6], x[7]));
+        const int mine = __shfl_sync(0xffffffffu, ue, (lane & 1) << 4);
+        if ((lane >> 1) == i) up = mine;
       }
-      zf = fp8::scale2(scale_log2, -up);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.q_full);
     }
-    const int row_slot = valid_q ? m.slots[row] : INT_MAX;
+    const float zf = fp8::scale2(scale_log2, -up);
+    const int row_slot = valid_q ? m.slots[row] : -1;
     const uint32_t* mrow =
         mask_words && valid_q ? mask_words + m.mask_word_indptr[row] : nullptr;
     const uint32_t lane_base = tmem + (uint32_t(quad * 32) << 16);
@@ -409,13 +465,32 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
                     (view.window == 0 || s0 > row_slot - view.window || s1 < view.sinks);
         }
         if (!__all_sync(0xffffffffu, all_vis || !valid_q)) {
+          // the visible columns as bits: a mask's own words, or ranges of slots
+          uint32_t see[2];
+          const int left = ke - ts;
 #pragma unroll
-          for (int c = 0; c < BN; ++c) {
-            const bool vis = valid_q && ts + c < ke &&
-                             (mask_words ? ((words[c >> 5] >> (c & 31)) & 1u) != 0
-                                         : view.sees(row_slot, view.slot(ts + c)));
-            s[c] = vis ? s[c] : -INFINITY;
+          for (int i = 0; i < 2; ++i) {
+            // (a 32-column half holds whole pages, so at most one change of pace)
+            const int h0 = view.slot(ts + 32 * i);
+            uint32_t w = words[i];
+            if (!mask_words) {
+              if (view.slot(ts + 32 * i + 31) - h0 == 31) {
+                w = low_bits(row_slot - h0 + 1);
+                if (view.window > 0) {
+                  const int first = max(0, row_slot - view.window + 1);
+                  w &= ~low_bits(first - h0) | low_bits(view.sinks - h0);
+                }
+              } else {
+                w = 0u;
+                for (int c = 0; c < 32; ++c)
+                  w |= view.sees(row_slot, view.slot(ts + 32 * i + c)) ? 1u << c : 0u;
+              }
+            }
+            see[i] = valid_q ? w & low_bits(left - 32 * i) : 0u;
           }
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (!((see[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
         }
         // the largest x = zf 2^ek s + ev (the factor stays above zero: the maximum of
         // 8 slots of one page commutes with it, and -inf stays -inf)

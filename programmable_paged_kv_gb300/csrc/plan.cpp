@@ -451,6 +451,42 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   const int64_t tc_target = 4 * static_cast<int64_t>(H.sms);
   int64_t tc_ch = tc_units >= tc_target ? INT32_MAX
                   : std::max<int64_t>(512, (tc_total + tc_target - 1) / tc_target);
+  // 8-bit caches and windows: the chunk that makes the time of the busiest SM
+  // shortest, an item costing its 64-slot tiles and about kItemTiles more (set-up,
+  // queries, the first copies, the outputs).  Few items run in whole waves;
+  // many balance, up to half of the longest one.
+  if ((H.kv8 || H.window > 0) && tc_units > 0) {
+    const int kItemTiles = 5;
+    static thread_local std::vector<int32_t> exts;
+    exts.clear();
+    int longest = 1;
+    for (int l = 0; l < L; ++l) {
+      if (!lane_tc(l)) continue;
+      const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1];
+      for (int b0 = r0; b0 < r1; b0 += tc_rows) {
+        int skip;
+        exts.push_back(reads(l, b0, std::min(r1, b0 + tc_rows), &skip));
+        longest = std::max(longest, exts.back());
+      }
+    }
+    double best = 0.0;
+    int best_n = 0;
+    for (int n = 1; n <= 64 && (n == 1 || longest / n >= 256); ++n) {
+      const int64_t ch = (longest + n - 1) / n;
+      int64_t items = 0, tiles = 0;
+      for (const int32_t e : exts) {
+        items += std::max<int64_t>(1, (e + ch / 2) / ch);
+        tiles += (e + 63) / 64;
+      }
+      items *= Hkv;
+      tiles *= Hkv;
+      const double mean = static_cast<double>(tiles) / items + kItemTiles;
+      const double cost = items <= 4 * static_cast<int64_t>(H.sms)
+                              ? std::ceil(static_cast<double>(items) / H.sms) * mean
+                              : mean * items / H.sms + 0.5 * (ch / 64 + kItemTiles);
+      if (best_n == 0 || cost < best) best = cost, best_n = n, tc_ch = ch;
+    }
+  }
   // (a masked item of an 8-bit cache lists its tiles in shared memory)
   if (H.kv8 && H.has_mask) tc_ch = std::min<int64_t>(tc_ch, 65536);
   H.comb.clear();
@@ -555,6 +591,11 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   if (H.dec_lists)
     std::stable_sort(H.dec.begin(), H.dec.end(), [](const DecItem& a, const DecItem& b) {
       return (a.block >= 0 ? a.kv_begin : 0) < (b.block >= 0 ? b.kv_begin : 0);
+    });
+  // the longest tensor-core items first, so that the short ones fill the end
+  if ((H.kv8 || H.window > 0) && !H.tc.empty())
+    std::stable_sort(H.tc.begin(), H.tc.end(), [](const TcItem& a, const TcItem& b) {
+      return a.kv_end - a.kv_begin > b.kv_end - b.kv_begin;
     });
   // readout positions per row (a row may be read out several times)
   H.ro_indptr.assign(N + 1, 0);
