@@ -31,13 +31,18 @@
 //     O^T come out in the order 0, 2, .. 14, 1, 3, .. 15 of each 16.
 // One CTA (4 compute warps and a producer warp) streams an item's chunk through a
 // ring of 64-slot stages, filled by tensor copies with a swizzle that keeps
-// ldmatrix free of bank conflicts.  Two warps share a stage, 32 slots each, and
-// the pairs take turns: at 2 d bytes per slot it is the issue slots that run
-// short, and two 16-slot units side by side share one softmax step's shuffles and
-// tests.  Units that every query vector sees in full skip the tests.  A persistent
-// grid takes items from a counter.  Items hold up to 8 query vectors (NT = 1: decode rows, bound by
-// HBM: a slot and kv head costs 2 d bytes) or 32 (NT = 4: drafts and prompts
-// that attend_kv8_tc.cu does not take, every code converted once for all of them).
+// ldmatrix free of bank conflicts; a persistent grid takes items from a counter.
+// Slots that every query vector of an item sees in full skip the tests.
+//   * Items of up to 8 query vectors (attend_kv8_kernel: decode rows, bound by HBM: a
+//     slot and kv head costs 2 d bytes): two warps share a stage, 32 slots each, and
+//     the pairs take turns; it is the issue slots that run short, and two
+//     16-slot units side by side share one softmax step's shuffles and tests.
+//     Every warp keeps its own state of all of d.
+//   * Items of up to 32 (attend_kv8_wide_kernel: drafts, and prompts that
+//     attend_kv8_tc.cu does not take): every code is converted once for all of
+//     them.  The warps split a stage by slots for the scores and by d for the
+//     output, with the weights handed over through shared memory and one running
+//     maximum for all four, so that a warp holds a quarter of O.
 // Masked passes skip stages that no row of the item sees.  Every wait is
 // bounded in time.
 
@@ -58,25 +63,26 @@ constexpr int THREADS = (WARPS + 1) * 32;
 constexpr int MAX_PAGES = kStageSlots / 8;  // pages per stage at most
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D, int NT, bool SPLIT>
+// Geometry of a kernel for items of NQ query vectors whose warps come to a stage in
+// groups of READERS.
+template <int D, int NQ, int READERS, bool SPLIT>
 struct Cfg {
   static constexpr int KS = D / 16;                      // 16-wide steps of d
   static constexpr int HALF = kStageSlots * D;           // K (or V) codes of a stage
   static constexpr int STAGE = 2 * HALF;
-  // 48 KB of ring per CTA at d 128: three CTAs per SM keep 144 KB in flight
+  // 48 KB of ring per CTA: three CTAs per SM keep 144 KB in flight
   static constexpr int STAGES = D == 128 ? 3 : 6;
-  // barriers of the stages: an even number, at least the ring's, so that each
-  // belongs to one pair of warps, which then sees every phase of it
-  static constexpr int BARS = (STAGES + 1) / 2 * 2;
+  // barriers of the stages: a multiple of the groups, at least the ring's, so that
+  // each belongs to one group, which then sees every phase of it (copies may
+  // complete in any order)
+  static constexpr int GROUPS = WARPS / READERS;
+  static constexpr int BARS = (STAGES + GROUPS - 1) / GROUPS * GROUPS;
   static constexpr int QROW = D * 2 + 32;                // fp16 query vector, padded by 32 bytes:
                                                          // 8 rows' 8-byte reads cover all banks
-  static constexpr int Q = 8 * NT * QROW * (SPLIT ? 2 : 1);
-  static constexpr int OROW = D + 4;                     // (float2 stores of 4 rows on distinct banks)
-  static constexpr int MERGE = WARPS * 8 * (OROW + 2) * 4;  // the warps' states of one query tile
+  static constexpr int Q = NQ * QROW * (SPLIT ? 2 : 1);
   static constexpr int SCALES = STAGES * 2 * MAX_PAGES * 4;
-  static constexpr int SMEM = STAGES * STAGE + Q + MERGE + SCALES + 8 * NT * 4 +
-                              (2 * BARS + 4) * 8 + 32 + 1024;
-  static constexpr int MIN_CTAS = NT == 1 ? 3 : 1;
+  // ring, query vectors, exponents, score factors, slots, barriers, item queue, alignment
+  static constexpr int BASE = STAGES * STAGE + Q + SCALES + NQ * 8 + (2 * BARS + 4) * 8 + 32 + 1024;
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
@@ -169,10 +175,258 @@ struct Stages {
   }
 };
 
+// What both kernels keep in shared memory, and the rest behind it.
+template <typename C>
+struct Shared {
+  uint8_t *ring, *qs, *rest;
+  int *exps, *qidx, *decision;
+  float* zq;
+  int* lim;
+  uint64_t *full, *empty, *item_full, *item_empty;
+  __device__ __forceinline__ Shared(uint8_t* raw, int nq) {
+    ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    qs = ring + C::STAGES * C::STAGE;                     // fp16 query vectors (then rests)
+    exps = reinterpret_cast<int*>(qs + C::Q);             // [STAGES][K, V][pages] exponents
+    zq = reinterpret_cast<float*>(exps + C::SCALES / 4);  // [nq] score factors
+    lim = reinterpret_cast<int*>(zq + nq);                // [nq] slots of their rows (-1: no vector)
+    full = reinterpret_cast<uint64_t*>(lim + nq);
+    empty = full + C::BARS;
+    item_full = empty + C::BARS;
+    item_empty = item_full + 2;
+    qidx = reinterpret_cast<int*>(item_empty + 2);
+    decision = qidx + 2;
+    rest = reinterpret_cast<uint8_t*>(decision + 6);
+  }
+  __device__ __forceinline__ void init(int readers) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < C::BARS; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], readers);
+      }
+      for (int q = 0; q < 2; ++q) {
+        mbar_init(&item_full[q], 1);
+        mbar_init(&item_empty[q], 1);
+      }
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
+};
+
+// The producer warp: takes items from the counter and streams their stages.  Lane
+// 2i + c copies the K (c = 0) or V (1) block of the stage's page i and, while
+// they are on their way, leaves its scale's exponent beside the stage.
+template <int D, typename C>
+__device__ __forceinline__ void produce(const Shared<C>& S, const DevMeta& m, int Hkv, int P,
+                                        const uint8_t* k_scale, const uint8_t* v_scale,
+                                        const uint32_t* mask_words, const DecItem* items,
+                                        int num_items, int* work, uint32_t* status,
+                                        uint64_t wait_ns, const CUtensorMap* kmap,
+                                        const CUtensorMap* vmap) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol = policy_evict_first();
+  const int c = lane & 1, pi = lane >> 1, lp = fp8::log2i(P), ppt = kStageSlots >> lp;
+  int gs = 0;  // stages issued by this CTA so far
+  // every way out counts the CTA done; the last one sets the counter back
+  auto finish = [&]() {
+    if (lane == 0) {
+      __threadfence();
+      if (atomicAdd(work + 1, 1) == int(gridDim.x) - 1) {
+        atomicExch(work, 0);
+        atomicExch(work + 1, 0);
+      }
+    }
+  };
+  int ticket = 0;  // lane 0: the next item, asked for while the last one streams
+  if (lane == 0) ticket = atomicAdd(work, 1);
+  for (int k = 0;; ++k) {
+    int idx = __shfl_sync(0xffffffffu, ticket, 0);
+    if (idx >= num_items) idx = -1;
+    const int q = k & 1;
+    if (k >= 2 && !mbar_wait_ns(&S.item_empty[q], ((k >> 1) - 1) & 1, wait_ns)) {
+      if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
+      break;
+    }
+    if (lane == 0) {
+      S.qidx[q] = idx;
+      mbar_arrive(&S.item_full[q]);
+    }
+    if (idx < 0) break;
+    if (lane == 0) ticket = atomicAdd(work, 1);
+    const DecItem it = items[idx];
+    Stages seen(m, mask_words, it);
+    const int i = pi < ppt ? pi : 0;
+    auto stage_at = [&](int j) { return it.kv_begin + j * kStageSlots; };
+    fp8::PageBatches pb(m, it.lane, window_pages(it.block), it.kv_head, it.kv_end, seen.n, Hkv, P,
+                        k_scale, v_scale, stage_at);
+    int next = seen.from(0);
+    for (int s = 0, ord = 0; s < seen.n; ++s) {
+      pb.at(s);
+      if (s != next) continue;
+      next = seen.from(s + 1);
+      // test hook: no copy of this or any later stage
+      const bool stop = ord == m.test_stall - 1;
+      ++ord;
+      // the stage that held this one's place in the ring has been read
+      const int st = gs % C::STAGES, before = gs - C::STAGES;
+      uint64_t* bar = &S.full[gs % C::BARS];
+      if (stop || (before >= 0 &&
+                   !mbar_wait_ns(&S.empty[before % C::BARS], (before / C::BARS) & 1, wait_ns))) {
+        if (!stop && lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
+        finish();
+        return;
+      }
+      const int pid = pb.page(s, i);
+      const bool issue = pi < ppt && pid >= 0;
+      const uint32_t copies = __popc(__ballot_sync(0xffffffffu, issue));
+      if (lane == 0) {
+        const int sb = stage_at(s);
+        if (copies != 2u * uint32_t(((min(sb + kStageSlots, it.kv_end) - 1) >> lp) - (sb >> lp) + 1))
+          set_status(status, PIE_STATUS_BOUNDS);
+        mbar_expect_tx(bar, copies * uint32_t(P) * D);
+      }
+      __syncwarp();
+      if (issue)
+        tma_3d(S.ring + st * C::STAGE + c * C::HALF + pi * P * D, c ? vmap : kmap,
+               int(int64_t(pid) * Hkv + it.kv_head), bar, pol);
+      const int ek = pb.k_exp(s, i), ev = pb.v_exp(s, i);
+      if (pi < MAX_PAGES) S.exps[(st * 2 + c) * MAX_PAGES + pi] = (c ? ev : ek) - fp8::kBias;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+      ++gs;
+    }
+  }
+  finish();
+}
+
+__device__ __forceinline__ void sync_compute() {
+  asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+}
+
+// The compute warps' k-th item (-1: none left, -2: the wait ran out), decided once.
+template <typename C>
+__device__ __forceinline__ int next_item(const Shared<C>& S, int k, uint32_t* status,
+                                         uint64_t wait_ns) {
+  if (threadIdx.x < 32) {
+    const int q = k & 1;
+    const bool ok = mbar_wait_ns(&S.item_full[q], (k >> 1) & 1, wait_ns);
+    int v = ok ? S.qidx[q] : -2;
+    v = __shfl_sync(0xffffffffu, v, 0);
+    if (threadIdx.x == 0) {
+      S.decision[k & 1] = v;
+      if (v != -2) mbar_arrive(&S.item_empty[q]);
+      else set_status(status, PIE_STATUS_TIMEOUT);
+    }
+  }
+  sync_compute();
+  return S.decision[k & 1];
+}
+
+// An item's query vectors, NQ of them, scaled into fp16's range by a power of two
+// each; 16 threads per vector.
+template <typename T, int D, int NQ, typename C>
+__device__ __forceinline__ void load_queries(const Shared<C>& S, const DevMeta& m, const DecItem& it,
+                                             const T* q_rot, int Hq, int G, float scale_log2) {
+  constexpr bool SPLIT = sizeof(T) == 4;
+  constexpr int EPT = D / 16;
+  const int ch = threadIdx.x & 15, nqv = it.nrows * G;
+#pragma unroll
+  for (int n = 0; n < NQ / 8; ++n) {
+    const int qv = n * 8 + (threadIdx.x >> 4);
+    float x[EPT];
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) x[e] = 0.f;
+    if (qv < nqv) {
+      const int row = it.row0 + qv / G, head = it.kv_head * G + qv % G;
+      const T* src = q_rot + (int64_t(row) * Hq + head) * D + ch * EPT;
+      if constexpr (sizeof(T) * EPT == 8) {
+        unpack8<T>(*reinterpret_cast<const uint2*>(src), x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPT; e += 16 / int(sizeof(T)))
+          unpack16<T>(*reinterpret_cast<const uint4*>(src + e), x + e);
+      }
+    }
+    float big = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) big = fmaxf(big, fabsf(x[e]));
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    const int up = fp8::query_exp(big);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) x[e] = fp8::scale2(x[e], up);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(S.qs + qv * C::QROW + ch * EPT * 2);
+#pragma unroll
+    for (int e = 0; e < EPT; e += 2) {
+      const uint32_t h = pack_half(x[e], x[e + 1]);
+      dst[e / 2] = h;
+      if constexpr (SPLIT) dst[NQ * C::QROW / 4 + e / 2] = pack_rest(x[e], x[e + 1], h);
+    }
+    if (ch == 0) {
+      S.zq[qv] = fp8::scale2(scale_log2, -up);
+      S.lim[qv] = qv < nqv ? m.slots[it.row0 + qv / G] : -1;
+    }
+  }
+}
+
+// Q^T fragments of step kk and query tile nt: d elements 16 kk + 4t .. 4t + 3 of
+// query 8 nt + g (and, for fp32, of the rests)
+template <int NQ, bool SPLIT, typename C>
+__device__ __forceinline__ void load_q(const Shared<C>& S, int nt, int kk, uint32_t* b) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t* src = S.qs + (nt * 8 + (lane >> 2)) * C::QROW + kk * 32 + (lane & 3) * 8;
+  const uint2 u = *reinterpret_cast<const uint2*>(src);
+  b[0] = u.x;
+  b[1] = u.y;
+  if constexpr (SPLIT) {
+    const uint2 w = *reinterpret_cast<const uint2*>(src + NQ * C::QROW);
+    b[2] = w.x;
+    b[3] = w.y;
+  }
+}
+
+// The slots that every query vector of an item sees.
+struct Common {
+  int lim_min, lim_max;
+  __device__ __forceinline__ Common(const int* lim, int nqv) {
+    const int lane = threadIdx.x & 31;
+    lim_min = __reduce_min_sync(0xffffffffu, lane < nqv ? lim[lane] : INT_MAX);
+    lim_max = __reduce_max_sync(0xffffffffu, lane < nqv ? lim[lane] : -1);
+  }
+  // positions [p0, p0 + n) of a view, whose slots rise with them
+  __device__ __forceinline__ bool all_see(const WindowView& view, int p0, int n) const {
+    const int s0 = view.slot(p0), s1 = view.slot(p0 + n - 1);
+    return s1 <= lim_min && (view.window == 0 || s0 > lim_max - view.window || s1 < view.sinks);
+  }
+};
+
+// V rows [first, first + n) of a stage become zero codes (rows past the end: their
+// zero weights then give zero); a whole warp
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* v, int first, int n) {
+  for (int i = threadIdx.x & 31; i < n * (D / 16); i += 32)
+    *reinterpret_cast<uint4*>(v + (first + i / (D / 16)) * D + i % (D / 16) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();  // the stage is later rewritten by the copy engine
+  __syncwarp();
+}
+
 }  // namespace a8
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::MIN_CTAS)
+// ---------------------------------------------------------------------------
+// items of up to 8 query vectors
+// ---------------------------------------------------------------------------
+namespace a8 {
+template <int D, bool SPLIT>
+struct NarrowCfg : Cfg<D, 8, 2, SPLIT> {
+  static constexpr int OROW = D + 4;                        // (float2 stores of 4 rows on distinct banks)
+  static constexpr int MERGE = WARPS * 8 * (OROW + 2) * 4;  // the warps' states
+  static constexpr int SMEM = NarrowCfg::BASE + MERGE;
+};
+}  // namespace a8
+
+template <typename T, int D>
+__global__ void __launch_bounds__(a8::THREADS, 3)
     attend_kv8_kernel(DevMeta m, int Hq, int Hkv, int G, int P, float scale_log2, const T* q_rot,
                       const uint8_t* k_scale, const uint8_t* v_scale, const uint32_t* mask_words,
                       const DecItem* items, int num_items, int* work, uint32_t* status,
@@ -180,507 +434,579 @@ __global__ void __launch_bounds__(a8::THREADS, a8::Cfg<D, NT, sizeof(T) == 4>::M
                       const __grid_constant__ CUtensorMap vmap) {
   using namespace a8;
   constexpr bool SPLIT = sizeof(T) == 4;
-  using C = Cfg<D, NT, SPLIT>;
+  using C = NarrowCfg<D, SPLIT>;
   constexpr int STAGES = C::STAGES, BARS = C::BARS, KS = C::KS;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint8_t* qs = ring + STAGES * C::STAGE;                        // fp16 query vectors (then rests)
-  float* merge = reinterpret_cast<float*>(qs + C::Q);            // [WARPS][8] m, l, then o
-  int* exps = reinterpret_cast<int*>(merge + C::MERGE / 4);      // [STAGES][K, V][pages] exponents
-  float* zq = reinterpret_cast<float*>(exps + C::SCALES / 4);    // [8 NT] score factors
-  uint64_t* full = reinterpret_cast<uint64_t*>(zq + 8 * NT);
-  uint64_t* empty = full + BARS;
-  uint64_t* item_full = empty + BARS;
-  uint64_t* item_empty = item_full + 2;
-  int* qidx = reinterpret_cast<int*>(item_empty + 2);
-  int* decision = qidx + 2;
+  Shared<C> S(smem_raw, 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < BARS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], WARPS / 2);  // the pair of warps that reads it
-    }
-    for (int q = 0; q < 2; ++q) {
-      mbar_init(&item_full[q], 1);
-      mbar_init(&item_empty[q], 1);
-    }
-    fence_barrier_init();
-  }
-  __syncthreads();
+  S.init(WARPS / 2);
   grid_dep_wait();
   grid_dep_launch();
   const uint64_t wait_ns = m.test_wait_us ? uint64_t(m.test_wait_us) * 1000ull : kWaitLimitNs;
-
   if (warp == WARPS) {
-    // ---------------- producer warp -----------------------------------------
-    // Lane 2i + c copies the K (c = 0) or V (1) block of the stage's page i and,
-    // while they are on their way, leaves its scale's exponent beside the stage.
-    const uint64_t pol = policy_evict_first();
-    const int c = lane & 1, pi = lane >> 1, lp = fp8::log2i(P), ppt = kStageSlots >> lp;
-    int gs = 0;  // stages issued by this CTA so far
-    // every way out counts the CTA done; the last one sets the counter back
-    auto finish = [&]() {
-      if (lane == 0) {
-        __threadfence();
-        if (atomicAdd(work + 1, 1) == int(gridDim.x) - 1) {
-          atomicExch(work, 0);
-          atomicExch(work + 1, 0);
-        }
-      }
-    };
-    int ticket = 0;  // lane 0: the next item, asked for while the last one streams
-    if (lane == 0) ticket = atomicAdd(work, 1);
-    for (int k = 0;; ++k) {
-      int idx = __shfl_sync(0xffffffffu, ticket, 0);
-      if (idx >= num_items) idx = -1;
-      const int q = k & 1;
-      if (k >= 2 && !mbar_wait_ns(&item_empty[q], ((k >> 1) - 1) & 1, wait_ns)) {
-        if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
-        finish();
-        return;
-      }
-      if (lane == 0) {
-        qidx[q] = idx;
-        mbar_arrive(&item_full[q]);
-      }
-      if (idx < 0) break;
-      if (lane == 0) ticket = atomicAdd(work, 1);
-      const DecItem it = items[idx];
-      Stages seen(m, mask_words, it);
-      auto issue_stage = [&](int ord, int s, int pid, int ek, int ev) -> bool {
-        if (ord == m.test_stall - 1) return false;  // test hook: nothing from here on
-        // the stage that held this one's place in the ring has been read
-        const int st = gs % STAGES, before = gs - STAGES;
-        uint64_t* bar = &full[gs % BARS];
-        if (before >= 0 && !mbar_wait_ns(&empty[before % BARS], (before / BARS) & 1, wait_ns)) {
-          if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
-          return false;
-        }
-        const bool issue = pi < ppt && pid >= 0;
-        const uint32_t copies = __popc(__ballot_sync(0xffffffffu, issue));
-        if (lane == 0) {
-          const int sb = it.kv_begin + s * kStageSlots;
-          if (copies != 2u * uint32_t(((min(sb + kStageSlots, it.kv_end) - 1) >> lp) - (sb >> lp) + 1))
-            set_status(status, PIE_STATUS_BOUNDS);
-          mbar_expect_tx(bar, copies * uint32_t(P) * D);
-        }
-        __syncwarp();
-        if (issue)
-          tma_3d(ring + st * C::STAGE + c * C::HALF + pi * P * D, c ? &vmap : &kmap,
-                 int(int64_t(pid) * Hkv + it.kv_head), bar, pol);
-        if (pi < MAX_PAGES) exps[(st * 2 + c) * MAX_PAGES + pi] = (c ? ev : ek) - fp8::kBias;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-        ++gs;
-        return true;
-      };
-      const int i = pi < ppt ? pi : 0;
-      auto stage_at = [&](int j) { return it.kv_begin + j * kStageSlots; };
-      fp8::PageBatches pb(m, it.lane, window_pages(it.block), it.kv_head, it.kv_end, seen.n, Hkv, P,
-                          k_scale, v_scale, stage_at);
-      int next = seen.from(0);
-      for (int s = 0, ord = 0; s < seen.n; ++s) {
-        pb.at(s);
-        if (s != next) continue;
-        const int pid = pb.page(s, i), ek = pb.k_exp(s, i), ev = pb.v_exp(s, i);
-        if (!issue_stage(ord, s, pid, ek, ev)) {
-          finish();
-          return;
-        }
-        ++ord;
-        next = seen.from(s + 1);
-      }
-    }
-    finish();
+    produce<D, C>(S, m, Hkv, P, k_scale, v_scale, mask_words, items, num_items, work, status, wait_ns,
+                  &kmap, &vmap);
     return;
   }
-
-  // ---------------- compute warps ---------------------------------------------
   // Fragments (g = lane / 4, t = lane % 4): scores S^T[slot g, g + 8][query 2t,
   // 2t + 1]; outputs O^T[d 16n + 2g, 16n + 2g + 1][query 2t, 2t + 1].
   const int g = lane >> 2, t = lane & 3;
   const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: lane i serves row i & 7 of matrix i >> 3
-  const uint32_t ring_s = smem_u32(ring);
+  const uint32_t ring_s = smem_u32(S.ring);
   const int half = (warp & 1) * 32, pair = warp >> 1, lp = fp8::log2i(P);
   int gs = 0;
   bool dead = false;  // a wait ran out: no more work, but every barrier is still taken
   for (int k = 0;; ++k) {
-    if (warp == 0) {
-      const int q = k & 1;
-      const bool ok = mbar_wait_ns(&item_full[q], (k >> 1) & 1, wait_ns);
-      int v = ok ? qidx[q] : -2;
-      v = __shfl_sync(0xffffffffu, v, 0);
-      if (lane == 0) {
-        decision[k & 1] = v;
-        if (v != -2) mbar_arrive(&item_empty[q]);
-        if (v == -2) set_status(status, PIE_STATUS_TIMEOUT);
-      }
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-    const int idx = decision[k & 1];
+    const int idx = next_item(S, k, status, wait_ns);
     if (idx < 0) break;
     const DecItem it = items[idx];
     const int nqv = it.nrows * G;
     const WindowView view(m, P, window_pages(it.block));
     Stages st_it(m, mask_words, it);
-
-    // the query vectors, scaled into fp16's range by a power of two each (the
-    // largest magnitude to [2^13, 2^14)); 16 threads per vector
-    {
-      constexpr int EPT = D / 16;
-      const int ch = threadIdx.x & 15;
+    load_queries<T, D, 8, C>(S, m, it, q_rot, Hq, G, scale_log2);
+    sync_compute();
+    const Common all(S.lim, nqv);
+    // this lane's query vectors 2t + i
+    int lim[2];
+    float zf[2];
+    const uint32_t* mrow[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int qv = nt * 8 + (threadIdx.x >> 4);
-        float x[EPT];
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) x[e] = 0.f;
-        if (qv < nqv) {
-          const int row = it.row0 + qv / G, head = it.kv_head * G + qv % G;
-          const T* src = q_rot + (int64_t(row) * Hq + head) * D + ch * EPT;
-          if constexpr (sizeof(T) * EPT == 8) {
-            unpack8<T>(*reinterpret_cast<const uint2*>(src), x);
-          } else {
-#pragma unroll
-            for (int e = 0; e < EPT; e += 16 / int(sizeof(T)))
-              unpack16<T>(*reinterpret_cast<const uint4*>(src + e), x + e);
-          }
-        }
-        float big = 0.f;
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) big = fmaxf(big, fabsf(x[e]));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-        const int up = fp8::query_exp(big);
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) x[e] = fp8::scale2(x[e], up);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(qs + qv * C::QROW + ch * EPT * 2);
-#pragma unroll
-        for (int e = 0; e < EPT; e += 2) {
-          const uint32_t h = pack_half(x[e], x[e + 1]);
-          dst[e / 2] = h;
-          if constexpr (SPLIT) dst[8 * NT * C::QROW / 4 + e / 2] = pack_rest(x[e], x[e + 1], h);
-        }
-        if (ch == 0) zq[qv] = fp8::scale2(scale_log2, -up);
-      }
+    for (int i = 0; i < 2; ++i) {
+      const int qv = 2 * t + i;
+      lim[i] = S.lim[qv];
+      zf[i] = S.zq[qv];
+      mrow[i] = mask_words && qv < nqv ? mask_words + m.mask_word_indptr[it.row0 + qv / G] : nullptr;
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-    // this lane's query vectors 8 nt + 2t + i; the slots that every one sees
-    bool valid_q[NT][2];
-    int slot_lim[NT][2];
-    float zf[NT][2];
-    const uint32_t* mrow[NT][2];
-    int lim_min = INT_MAX, lim_max = -1;
+    // (one bf16 query tile stays in registers)
+    uint32_t qb[SPLIT ? 1 : KS][2];
+    if constexpr (!SPLIT) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int qv = nt * 8 + 2 * t + i;
-        valid_q[nt][i] = qv < nqv;
-        const int row = it.row0 + (valid_q[nt][i] ? qv : 0) / G;
-        slot_lim[nt][i] = valid_q[nt][i] ? m.slots[row] : -1;
-        if (valid_q[nt][i]) {
-          lim_min = min(lim_min, slot_lim[nt][i]);
-          lim_max = max(lim_max, slot_lim[nt][i]);
-        }
-        zf[nt][i] = zq[qv];
-        mrow[nt][i] = valid_q[nt][i] && mask_words ? mask_words + m.mask_word_indptr[row] : nullptr;
-      }
-    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-    lim_max = __reduce_max_sync(0xffffffffu, lim_max);
-    // Q^T fragments: d elements 16k + 4t .. 4t + 3 of query g (one bf16 query
-    // tile keeps them in registers)
-    constexpr bool QREG = NT == 1 && !SPLIT;
-    uint32_t qb[QREG ? KS : 1][2];
-    auto load_q = [&](int nt, int kk, uint32_t* b) {
-      const uint8_t* src = qs + (nt * 8 + g) * C::QROW + kk * 32 + t * 8;
-      const uint2 u = *reinterpret_cast<const uint2*>(src);
-      b[0] = u.x;
-      b[1] = u.y;
-      if constexpr (SPLIT) {
-        const uint2 w = *reinterpret_cast<const uint2*>(src + 8 * NT * C::QROW);
-        b[2] = w.x;
-        b[3] = w.y;
-      }
-    };
-    if constexpr (QREG) {
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) load_q(0, kk, qb[kk]);
+      for (int kk = 0; kk < KS; ++kk) load_q<8, false, C>(S, 0, kk, qb[kk]);
     }
-    float o[NT][KS][4];
-    float m_used[NT][2], l_part[NT][2];
+    float o[KS][4];
+    float m_used[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int n = 0; n < KS; ++n) o[nt][n][0] = o[nt][n][1] = o[nt][n][2] = o[nt][n][3] = 0.f;
-      m_used[nt][0] = m_used[nt][1] = -INFINITY;
-      l_part[nt][0] = l_part[nt][1] = 0.f;
-    }
+    for (int n = 0; n < KS; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
     for (int s = st_it.from(0); s < st_it.n; s = st_it.from(s + 1), ++gs) {
       if ((gs & 1) != pair || dead) continue;  // the other pair's stage
       const int st = gs % STAGES;
       const int base = it.kv_begin + s * kStageSlots + half;  // this warp's first position
-      const int left = it.kv_end - base;
+      const int nvalid = min(32, it.kv_end - base);
       // the rows' mask words of these positions, on their way while the stage lands
-      uint32_t word[NT][2];
+      uint32_t word[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) word[nt][i] = mrow[nt][i] && left > 0 ? mrow[nt][i][base >> 5] : ~0u;
-      if (!mbar_wait_ns(&full[gs % BARS], (gs / BARS) & 1, wait_ns)) {
+      for (int i = 0; i < 2; ++i) word[i] = mrow[i] && nvalid > 0 ? mrow[i][base >> 5] : 0u;
+      if (!mbar_wait_ns(&S.full[gs % BARS], (gs / BARS) & 1, wait_ns)) {
         dead = true;
         if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
         continue;
       }
-      // U units of 16 slots side by side: two, or one after the other where the
-      // query tiles take the registers
-      constexpr int U = NT == 1 ? 2 : 1;
-#pragma unroll 1
-      for (int u0 = 0; u0 < 2 && left > 16 * u0; u0 += U) {
-        const int unit = half + 16 * u0;  // first row within the stage
-        const int ub = base + 16 * u0;
-        const int nvalid = min(16 * U, left - 16 * u0);
+      if (nvalid > 0) {
         const uint32_t kbase = ring_s + st * C::STAGE, vbase = kbase + C::HALF;
-        if (nvalid < 16 * U) {
-          // V rows past the end: zero codes, so that their zero weights give zero
-          for (int i = lane; i < (16 * U - nvalid) * (D / 16); i += 32)
-            *reinterpret_cast<uint4*>(ring + st * C::STAGE + C::HALF +
-                                      (unit + nvalid + i / (D / 16)) * D + i % (D / 16) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();  // the stage is later rewritten by the copy engine
-          __syncwarp();
-        }
-        // ---- S^T = K Q^T: matrices (slots 0-7, chunk 2kk), (8-15, 2kk),
-        // (0-7, 2kk + 1), (8-15, 2kk + 1)
-        float cc[U][NT][4];
+        if (nvalid < 32) zero_rows<D>(S.ring + st * C::STAGE + C::HALF, half + nvalid, 32 - nvalid);
+        // ---- S^T = K Q^T for two units of 16 slots: matrices (slots 0-7, chunk kk),
+        // (8-15, kk), (0-7, kk + 1), (8-15, kk + 1)
+        float cc[2][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            cc[u][nt][0] = cc[u][nt][1] = cc[u][nt][2] = cc[u][nt][3] = 0.f;
+        for (int u = 0; u < 2; ++u) cc[u][0] = cc[u][1] = cc[u][2] = cc[u][3] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KS; kk += 2) {
-          uint32_t w[U][4];
+          uint32_t w[2][4];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            ldsm_x4(kbase + chunk<D>(unit + 16 * u + (mi & 1) * 8 + mr, kk + (mi >> 1)), w[u]);
+          for (int u = 0; u < 2; ++u)
+            ldsm_x4(kbase + chunk<D>(half + 16 * u + (mi & 1) * 8 + mr, kk + (mi >> 1)), w[u]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t a[U][4];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              fp8::to_half2x2(w[u][2 * h], a[u][0], a[u][2]);
-              fp8::to_half2x2(w[u][2 * h + 1], a[u][1], a[u][3]);
+            uint32_t b[SPLIT ? 4 : 2];
+            if constexpr (SPLIT) {
+              load_q<8, true, C>(S, 0, kk + h, b);
+            } else {
+              b[0] = qb[kk + h][0];
+              b[1] = qb[kk + h][1];
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t b[SPLIT ? 4 : 2];
-              if constexpr (QREG) {
-                b[0] = qb[kk + h][0];
-                b[1] = qb[kk + h][1];
-              } else {
-                load_q(nt, kk + h, b);
-              }
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
-                mma(cc[u][nt], a[u], b[0], b[1]);
-                if constexpr (SPLIT) mma(cc[u][nt], a[u], b[2], b[3]);
-              }
+            for (int u = 0; u < 2; ++u) {
+              uint32_t a[4];
+              fp8::to_half2x2(w[u][2 * h], a[0], a[2]);
+              fp8::to_half2x2(w[u][2 * h + 1], a[1], a[3]);
+              mma(cc[u], a, b[0], b[1]);
+              if constexpr (SPLIT) mma(cc[u], a, b[2], b[3]);
             }
           }
         }
-        // this lane's slots g and g + 8 of each unit: their pages' scales
-        float sk[U][2], unsv[U][2], lv[U][2];
+        if (mask_words || nvalid < 32 || !all.all_see(view, base, 32)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int pg = (unit + 16 * u + g + 8 * j) >> lp;
-            const int ek = exps[st * 2 * MAX_PAGES + pg], ev = exps[(st * 2 + 1) * MAX_PAGES + pg];
-            sk[u][j] = fp8::pow2i(ek);
-            unsv[u][j] = fp8::pow2i(-ev);
-            lv[u][j] = float(ev);
-          }
-        // positions that every query vector sees (slots rise with them)
-        const int s0 = view.slot(ub), s1 = view.slot(ub + 16 * U - 1);
-        const bool all = !mask_words && nvalid == 16 * U && s1 <= lim_min &&
-                         (view.window == 0 || s0 > lim_max - view.window || s1 < view.sinks);
-        if (!all) {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = e & 1, cs = 16 * u + g + 8 * (e >> 1);
-                const bool vis = valid_q[nt][i] && cs < nvalid &&
-                                 (mrow[nt][i] ? ((word[nt][i] >> (16 * u0 + cs)) & 1u) != 0
-                                              : view.sees(slot_lim[nt][i], view.slot(ub + cs)));
-                if (!vis) cc[u][nt][e] = -INFINITY;
-              }
-        }
-        uint32_t pb[U][NT][SPLIT ? 4 : 2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // cc[u][nt][e]: slot 16u + g + 8 (e >> 1), query 2t + (e & 1); the
-          // factors stay above zero, so that -inf stays -inf
-          float zs[U][4], mt[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int u = 0; u < U; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              zs[u][e] = fmaxf(zf[nt][e & 1] * sk[u][e >> 1], FLT_MIN);
-              mt[e & 1] = fmaxf(mt[e & 1], fmaf(cc[u][nt][e], zs[u][e], lv[u][e >> 1]));
+              const int i = e & 1, cs = 16 * u + g + 8 * (e >> 1);
+              const bool vis = cs < nvalid && (mask_words ? ((word[i] >> cs) & 1u) != 0
+                                                          : view.sees(lim[i], view.slot(base + cs)));
+              if (!vis) cc[u][e] = -INFINITY;
             }
+        }
+        // this lane's slots g and g + 8 of each unit: their pages' scales; cc[u][e]:
+        // slot 16u + g + 8 (e >> 1), query 2t + (e & 1).  The factors stay above
+        // zero, so that -inf stays -inf.
+        float unsv[2][2], lv[2][2], zs[2][4], mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) {
-            mt[0] = fmaxf(mt[0], __shfl_xor_sync(0xffffffffu, mt[0], off));
-            mt[1] = fmaxf(mt[1], __shfl_xor_sync(0xffffffffu, mt[1], off));
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int pg = (half + 16 * u + g + 8 * j) >> lp;
+            const int ek = S.exps[st * 2 * MAX_PAGES + pg], ev = S.exps[(st * 2 + 1) * MAX_PAGES + pg];
+            unsv[u][j] = fp8::pow2i(-ev);
+            lv[u][j] = float(ev);
+            zs[u][2 * j] = fmaxf(zf[0] * fp8::pow2i(ek), FLT_MIN);
+            zs[u][2 * j + 1] = fmaxf(zf[1] * fp8::pow2i(ek), FLT_MIN);
           }
-          // (m_used + 8 is -inf at first: any visible score moves it)
-          if (__any_sync(0xffffffffu, mt[0] > m_used[nt][0] + 8.f || mt[1] > m_used[nt][1] + 8.f)) {
-            float alpha[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float m_new = mt[i] > m_used[nt][i] + 8.f ? ceilf(mt[i]) : m_used[nt][i];
-              alpha[i] = m_new == m_used[nt][i] ? 1.f : ex2(m_used[nt][i] - m_new);
-              l_part[nt][i] *= alpha[i];
-              m_used[nt][i] = m_new;
-            }
+          for (int e = 0; e < 4; ++e)
+            mt[e & 1] = fmaxf(mt[e & 1], fmaf(cc[u][e], zs[u][e], lv[u][e >> 1]));
+        }
 #pragma unroll
-            for (int n = 0; n < KS; ++n) {
-              o[nt][n][0] *= alpha[0];
-              o[nt][n][1] *= alpha[1];
-              o[nt][n][2] *= alpha[0];
-              o[nt][n][3] *= alpha[1];
-            }
+        for (int off = 4; off < 32; off <<= 1) {
+          mt[0] = fmaxf(mt[0], __shfl_xor_sync(0xffffffffu, mt[0], off));
+          mt[1] = fmaxf(mt[1], __shfl_xor_sync(0xffffffffu, mt[1], off));
+        }
+        // (m_used + 8 is -inf at first: any visible score moves it)
+        if (__any_sync(0xffffffffu, mt[0] > m_used[0] + 8.f || mt[1] > m_used[1] + 8.f)) {
+          float alpha[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float m_new = mt[i] > m_used[i] + 8.f ? ceilf(mt[i]) : m_used[i];
+            alpha[i] = m_new == m_used[i] ? 1.f : ex2(m_used[i] - m_new);
+            l_part[i] *= alpha[i];
+            m_used[i] = m_new;
           }
-          // (no visible slot yet: every score is -inf, and so is every exponent)
-          const float neg_m[2] = {m_used[nt][0] == -INFINITY ? 0.f : -m_used[nt][0],
-                                  m_used[nt][1] == -INFINITY ? 0.f : -m_used[nt][1]};
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            float p[4];
+          for (int n = 0; n < KS; ++n) {
+            o[n][0] *= alpha[0];
+            o[n][1] *= alpha[1];
+            o[n][2] *= alpha[0];
+            o[n][3] *= alpha[1];
+          }
+        }
+        // (no visible slot yet: every score is -inf, and so is every exponent)
+        const float neg_m[2] = {m_used[0] == -INFINITY ? 0.f : -m_used[0],
+                                m_used[1] == -INFINITY ? 0.f : -m_used[1]};
+        uint32_t pb[2][SPLIT ? 4 : 2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              p[e] = ex2(fmaf(cc[u][nt][e], zs[u][e], lv[u][e >> 1] + neg_m[e & 1]));
-            l_part[nt][0] = fmaf(p[0], unsv[u][0], fmaf(p[2], unsv[u][1], l_part[nt][0]));
-            l_part[nt][1] = fmaf(p[1], unsv[u][0], fmaf(p[3], unsv[u][1], l_part[nt][1]));
-            const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
-            pb[u][nt][0] = movmatrix_t(h0);
-            pb[u][nt][1] = movmatrix_t(h1);
-            if constexpr (SPLIT) {
-              pb[u][nt][2] = movmatrix_t(pack_rest(p[0], p[1], h0));
-              pb[u][nt][3] = movmatrix_t(pack_rest(p[2], p[3], h1));
-            }
+        for (int u = 0; u < 2; ++u) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p[e] = ex2(fmaf(cc[u][e], zs[u][e], lv[u][e >> 1] + neg_m[e & 1]));
+          l_part[0] = fmaf(p[0], unsv[u][0], fmaf(p[2], unsv[u][1], l_part[0]));
+          l_part[1] = fmaf(p[1], unsv[u][0], fmaf(p[3], unsv[u][1], l_part[1]));
+          const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
+          pb[u][0] = movmatrix_t(h0);
+          pb[u][1] = movmatrix_t(h1);
+          if constexpr (SPLIT) {
+            pb[u][2] = movmatrix_t(pack_rest(p[0], p[1], h0));
+            pb[u][3] = movmatrix_t(pack_rest(p[2], p[3], h1));
           }
         }
         // ---- O^T += V^T P^T: matrices (slots 0-7, chunk n), (8-15, n), (0-7,
         // n + 1), (8-15, n + 1), transposed
 #pragma unroll
         for (int n = 0; n < KS; n += 2) {
-          uint32_t w[U][4];
+          uint32_t w[2][4];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            ldsm_x4_t(vbase + chunk<D>(unit + 16 * u + (mi & 1) * 8 + mr, n + (mi >> 1)), w[u]);
+          for (int u = 0; u < 2; ++u)
+            ldsm_x4_t(vbase + chunk<D>(half + 16 * u + (mi & 1) * 8 + mr, n + (mi >> 1)), w[u]);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < 2; ++u) {
               uint32_t a[4];
               fp8::to_half2x2(__byte_perm(w[u][2 * h], 0, 0x3120), a[0], a[1]);
               fp8::to_half2x2(__byte_perm(w[u][2 * h + 1], 0, 0x3120), a[2], a[3]);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma(o[nt][n + h], a, pb[u][nt][0], pb[u][nt][1]);
-                if constexpr (SPLIT) mma(o[nt][n + h], a, pb[u][nt][2], pb[u][nt][3]);
-              }
+              mma(o[n + h], a, pb[u][0], pb[u][1]);
+              if constexpr (SPLIT) mma(o[n + h], a, pb[u][2], pb[u][3]);
             }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[gs % BARS]);
+      if (lane == 0) mbar_arrive(&S.empty[gs % BARS]);
     }
 
-    // ---- merge the warps' states into the item's partials, a query tile at a
-    // time (the buffer's last readers have passed the barriers since)
-    float* mw = merge;            // [WARPS][8]
-    float* lw = mw + WARPS * 8;   // [WARPS][8]
-    float* ow = lw + WARPS * 8;   // [WARPS][8][OROW]
+    // ---- merge the warps' states into the item's partials (the buffer's last
+    // readers have passed two barriers since)
+    float* mw = reinterpret_cast<float*>(S.rest);  // [WARPS][8]
+    float* lw = mw + WARPS * 8;                    // [WARPS][8]
+    float* ow = lw + WARPS * 8;                    // [WARPS][8][OROW]
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt * 8 >= nqv) break;
-      if (nt > 0) asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+    for (int i = 0; i < 2; ++i) {
+      float l = l_part[i];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float l = l_part[nt][i];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        const int q = 2 * t + i;
-        if (g == 0) {
-          mw[warp * 8 + q] = m_used[nt][i];
-          lw[warp * 8 + q] = l;
-        }
-        float* orow = ow + (warp * 8 + q) * C::OROW;
-#pragma unroll
-        for (int n = 0; n < KS; ++n)
-          *reinterpret_cast<float2*>(orow + 16 * n + 2 * g) = make_float2(o[nt][n][i], o[nt][n][2 + i]);
+      for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      const int q = 2 * t + i;
+      if (g == 0) {
+        mw[warp * 8 + q] = m_used[i];
+        lw[warp * 8 + q] = l;
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-      for (int i = threadIdx.x; i < min(8, nqv - nt * 8) * D; i += WARPS * 32) {
-        const int qq = i / D, cd = i % D;
-        float M = -INFINITY;
+      float* orow = ow + (warp * 8 + q) * C::OROW;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mw[w * 8 + qq]);
-        float O = 0.f, L = 0.f;
-        if (M != -INFINITY) {
+      for (int n = 0; n < KS; ++n)
+        *reinterpret_cast<float2*>(orow + 16 * n + 2 * g) = make_float2(o[n][i], o[n][2 + i]);
+    }
+    sync_compute();
+    for (int i = threadIdx.x; i < nqv * D; i += WARPS * 32) {
+      const int qq = i / D, cd = i % D;
+      float M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < WARPS; ++w) {
-            const float mv = mw[w * 8 + qq];
-            const float f = mv == -INFINITY ? 0.f : ex2(mv - M);
-            O = fmaf(f, ow[(w * 8 + qq) * C::OROW + cd], O);
-            L = fmaf(f, lw[w * 8 + qq], L);
-          }
+      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mw[w * 8 + qq]);
+      float O = 0.f, Ls = 0.f;
+      if (M != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float mv = mw[w * 8 + qq];
+          const float f = mv == -INFINITY ? 0.f : ex2(mv - M);
+          O = fmaf(f, ow[(w * 8 + qq) * C::OROW + cd], O);
+          Ls = fmaf(f, lw[w * 8 + qq], Ls);
         }
-        const int64_t at = int64_t(it.part_base) + nt * 8 + qq;
-        m.part_o[at * D + cd] = O;
-        if (cd == 0) m.part_ml[at] = make_float2(M, L);
       }
+      const int64_t at = int64_t(it.part_base) + qq;
+      m.part_o[at * D + cd] = O;
+      if (cd == 0) m.part_ml[at] = make_float2(M, Ls);
     }
   }
 }
 
-template <typename T, int D, int NT>
+// ---------------------------------------------------------------------------
+// items of up to 32 query vectors
+// ---------------------------------------------------------------------------
+namespace a8 {
+template <int D, bool SPLIT>
+struct WideCfg : Cfg<D, kWideQueries, WARPS, SPLIT> {
+  // weights [query][slot] in fp16, rows padded by 16 bytes (ldmatrix and the
+  // writers' stores hit distinct banks), and their rests for fp32
+  static constexpr int PROW = kStageSlots * 2 + 16;
+  static constexpr int PBUF = kWideQueries * PROW;
+  static constexpr int EXCH = WARPS * kWideQueries * 4;  // the warps' maxima, later their sums
+  static constexpr int SMEM = WideCfg::BASE + PBUF * (SPLIT ? 2 : 1) + EXCH;
+};
+
+// a barrier of the compute warps that tells whether any thread says so
+__device__ __forceinline__ bool sync_or(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q, p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(p)), "n"(WARPS * 32)
+      : "memory");
+  return r != 0;
+}
+}  // namespace a8
+
+template <typename T, int D>
+__global__ void __launch_bounds__(a8::THREADS, 3)
+    attend_kv8_wide_kernel(DevMeta m, int Hq, int Hkv, int G, int P, float scale_log2, const T* q_rot,
+                           const uint8_t* k_scale, const uint8_t* v_scale,
+                           const uint32_t* mask_words, const DecItem* items, int num_items, int* work,
+                           uint32_t* status, const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap) {
+  using namespace a8;
+  constexpr bool SPLIT = sizeof(T) == 4;
+  using C = WideCfg<D, SPLIT>;
+  constexpr int STAGES = C::STAGES, KS = C::KS, NT = kWideQueries / 8;
+  constexpr int CH = KS / WARPS;  // 16-wide tiles of d per warp
+  static_assert(C::BARS == STAGES, "every warp sees every stage");
+  extern __shared__ uint8_t smem_raw[];
+  Shared<C> S(smem_raw, kWideQueries);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  S.init(WARPS);
+  grid_dep_wait();
+  grid_dep_launch();
+  const uint64_t wait_ns = m.test_wait_us ? uint64_t(m.test_wait_us) * 1000ull : kWaitLimitNs;
+  if (warp == WARPS) {
+    produce<D, C>(S, m, Hkv, P, k_scale, v_scale, mask_words, items, num_items, work, status, wait_ns,
+                  &kmap, &vmap);
+    return;
+  }
+  // Fragments as above, for query tiles nt: scores S^T[slot 16w + g, + 8][query 8 nt +
+  // 2t, + 1] of warp w; outputs O^T[d 16 (CH w + n) + 2g, + 1][the same queries].
+  const int g = lane >> 2, t = lane & 3;
+  const int mi = lane >> 3, mr = lane & 7;
+  const uint32_t ring_s = smem_u32(S.ring);
+  uint8_t* pbuf = S.rest;
+  const uint32_t pbuf_s = smem_u32(pbuf);
+  float* exch = reinterpret_cast<float*>(pbuf + C::PBUF * (SPLIT ? 2 : 1));  // [WARPS][32]
+  const int unit = warp * kWarpSlots, lp = fp8::log2i(P);
+  int gs = 0;
+  bool dead = false;  // a wait ran out: no more work, but every barrier is still taken
+  for (int k = 0;; ++k) {
+    const int idx = next_item(S, k, status, wait_ns);
+    if (idx < 0) break;
+    const DecItem it = items[idx];
+    const int nqv = it.nrows * G;
+    const WindowView view(m, P, window_pages(it.block));
+    Stages st_it(m, mask_words, it);
+    load_queries<T, D, kWideQueries, C>(S, m, it, q_rot, Hq, G, scale_log2);
+    sync_compute();
+    const Common all(S.lim, nqv);
+    float o[NT][CH][4];
+    float m_used[NT][2], l_part[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int n = 0; n < CH; ++n) o[nt][n][0] = o[nt][n][1] = o[nt][n][2] = o[nt][n][3] = 0.f;
+      m_used[nt][0] = m_used[nt][1] = -INFINITY;
+      l_part[nt][0] = l_part[nt][1] = 0.f;
+    }
+
+    for (int s = st_it.from(0); s < st_it.n; s = st_it.from(s + 1), ++gs) {
+      const int st = gs % STAGES;
+      const int base = it.kv_begin + s * kStageSlots + unit;  // this warp's first position
+      const int nvalid = max(0, min(kWarpSlots, it.kv_end - base));
+      if (!dead && !mbar_wait_ns(&S.full[gs % C::BARS], (gs / C::BARS) & 1, wait_ns)) {
+        dead = true;
+        if (lane == 0) set_status(status, PIE_STATUS_TIMEOUT);
+      }
+      const uint32_t kbase = ring_s + st * C::STAGE, vbase = kbase + C::HALF;
+      if (nvalid < kWarpSlots && !dead)
+        zero_rows<D>(S.ring + st * C::STAGE + C::HALF, unit + nvalid, kWarpSlots - nvalid);
+      // ---- S^T = K Q^T for this warp's 16 slots
+      float cc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) cc[nt][0] = cc[nt][1] = cc[nt][2] = cc[nt][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < KS; kk += 2) {
+        uint32_t w[4];
+        ldsm_x4(kbase + chunk<D>(unit + (mi & 1) * 8 + mr, kk + (mi >> 1)), w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[4];
+          fp8::to_half2x2(w[2 * h], a[0], a[2]);
+          fp8::to_half2x2(w[2 * h + 1], a[1], a[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t b[SPLIT ? 4 : 2];
+            load_q<kWideQueries, SPLIT, C>(S, nt, kk + h, b);
+            mma(cc[nt], a, b[0], b[1]);
+            if constexpr (SPLIT) mma(cc[nt], a, b[2], b[3]);
+          }
+        }
+      }
+      if (mask_words || nvalid < kWarpSlots || !all.all_see(view, base, kWarpSlots)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int qv = nt * 8 + 2 * t + i, lim = S.lim[qv];
+            uint32_t word = 0u;
+            if (mask_words && qv < nqv && nvalid > 0)
+              word = mask_words[m.mask_word_indptr[it.row0 + qv / G] + (base >> 5)] >> (base & 31);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int cs = g + 8 * j;
+              const bool vis = cs < nvalid && (mask_words ? ((word >> cs) & 1u) != 0
+                                                          : view.sees(lim, view.slot(base + cs)));
+              if (!vis) cc[nt][2 * j + i] = -INFINITY;
+            }
+          }
+      }
+      float sk[2], unsv[2], lv[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int pg = (unit + g + 8 * j) >> lp;
+        const int ek = S.exps[st * 2 * MAX_PAGES + pg], ev = S.exps[(st * 2 + 1) * MAX_PAGES + pg];
+        sk[j] = fp8::pow2i(ek);
+        unsv[j] = fp8::pow2i(-ev);
+        lv[j] = float(ev);
+      }
+      // ---- one running maximum for all warps: it moves only where some warp's
+      // scores exceed it by more than 2^8, and only then are maxima exchanged
+      float mt[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 z = *reinterpret_cast<const float2*>(S.zq + nt * 8 + 2 * t);
+        const float zf[2] = {z.x, z.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          mt[nt][i] = fmaxf(fmaf(cc[nt][i], fmaxf(zf[i] * sk[0], FLT_MIN), lv[0]),
+                            fmaf(cc[nt][2 + i], fmaxf(zf[i] * sk[1], FLT_MIN), lv[1]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) grow = grow || mt[nt][i] > m_used[nt][i] + 8.f;
+      }
+      // (also: every warp has read the last stage's weights)
+      if (sync_or(grow && !dead)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = mt[nt][i];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+            if (g == 0) exch[warp * kWideQueries + nt * 8 + 2 * t + i] = x;
+          }
+        sync_compute();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int q = nt * 8 + 2 * t + i;
+            float x = exch[q];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) x = fmaxf(x, exch[w * kWideQueries + q]);
+            const float m_new = x > m_used[nt][i] + 8.f ? ceilf(x) : m_used[nt][i];
+            alpha[i] = m_new == m_used[nt][i] ? 1.f : ex2(m_used[nt][i] - m_new);
+            l_part[nt][i] *= alpha[i];
+            m_used[nt][i] = m_new;
+          }
+#pragma unroll
+          for (int n = 0; n < CH; ++n) {
+            o[nt][n][0] *= alpha[0];
+            o[nt][n][1] *= alpha[1];
+            o[nt][n][2] *= alpha[0];
+            o[nt][n][3] *= alpha[1];
+          }
+        }
+      }
+      // ---- weights, handed over as P[query][slot]
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 z = *reinterpret_cast<const float2*>(S.zq + nt * 8 + 2 * t);
+        const float zf[2] = {z.x, z.y};
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mu = m_used[nt][e & 1], neg_m = mu == -INFINITY ? 0.f : -mu;
+          p[e] = ex2(fmaf(cc[nt][e], fmaxf(zf[e & 1] * sk[e >> 1], FLT_MIN), lv[e >> 1] + neg_m));
+        }
+        l_part[nt][0] = fmaf(p[0], unsv[0], fmaf(p[2], unsv[1], l_part[nt][0]));
+        l_part[nt][1] = fmaf(p[1], unsv[0], fmaf(p[3], unsv[1], l_part[nt][1]));
+        const uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
+        // transposed: query 8 nt + g, slots 2t, 2t + 1 (and + 8) of this warp's 16
+        uint8_t* row = pbuf + (nt * 8 + g) * C::PROW + (unit + 2 * t) * 2;
+        *reinterpret_cast<uint32_t*>(row) = movmatrix_t(h0);
+        *reinterpret_cast<uint32_t*>(row + 16) = movmatrix_t(h1);
+        if constexpr (SPLIT) {
+          *reinterpret_cast<uint32_t*>(row + C::PBUF) = movmatrix_t(pack_rest(p[0], p[1], h0));
+          *reinterpret_cast<uint32_t*>(row + C::PBUF + 16) = movmatrix_t(pack_rest(p[2], p[3], h1));
+        }
+      }
+      sync_compute();
+      // ---- O^T += V^T P^T for this warp's tiles of d, 32 slots at a time: the
+      // weights' fragments for 16 slots are matrices (queries, slots 0-7), (8-15)
+#pragma unroll
+      for (int ks = 0; ks < kStageSlots; ks += 32) {
+        uint32_t pf[NT][4], pr[SPLIT ? NT : 1][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t at = pbuf_s + (nt * 8 + mr) * C::PROW + (ks + 8 * mi) * 2;
+          ldsm_x4(at, pf[nt]);
+          if constexpr (SPLIT) ldsm_x4(at + C::PBUF, pr[nt]);
+        }
+        // V^T fragments a[u][n]: 16 slots u, tile n of this warp's
+        uint32_t a[2][CH][4];
+        if constexpr (CH == 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t w[4];
+            ldsm_x4_t(vbase + chunk<D>(ks + 16 * u + (mi & 1) * 8 + mr, 2 * warp + (mi >> 1)), w);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              fp8::to_half2x2(__byte_perm(w[2 * n], 0, 0x3120), a[u][n][0], a[u][n][1]);
+              fp8::to_half2x2(__byte_perm(w[2 * n + 1], 0, 0x3120), a[u][n][2], a[u][n][3]);
+            }
+          }
+        } else {
+          uint32_t w[4];
+          ldsm_x4_t(vbase + chunk<D>(ks + 8 * mi + mr, warp), w);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            fp8::to_half2x2(__byte_perm(w[2 * u], 0, 0x3120), a[u][0][0], a[u][0][1]);
+            fp8::to_half2x2(__byte_perm(w[2 * u + 1], 0, 0x3120), a[u][0][2], a[u][0][3]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int n = 0; n < CH; ++n)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(o[nt][n], a[u][n], pf[nt][2 * u], pf[nt][2 * u + 1]);
+              if constexpr (SPLIT) mma(o[nt][n], a[u][n], pr[nt][2 * u], pr[nt][2 * u + 1]);
+            }
+      }
+      __syncwarp();
+      if (lane == 0 && !dead) mbar_arrive(&S.empty[gs % C::BARS]);
+    }
+
+    // ---- the item's partials: every warp its tiles of d, the sums together
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int q = nt * 8 + 2 * t + i;
+        float l = l_part[nt][i];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (g == 0) exch[warp * kWideQueries + q] = l;
+        if (q < nqv) {
+          float* po = m.part_o + (int64_t(it.part_base) + q) * D + 16 * CH * warp + 2 * g;
+#pragma unroll
+          for (int n = 0; n < CH; ++n)
+            *reinterpret_cast<float2*>(po + 16 * n) = make_float2(o[nt][n][i], o[nt][n][2 + i]);
+        }
+      }
+    sync_compute();
+    if (warp == 0 && g == 0)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int q = nt * 8 + 2 * t + i;
+          float l = 0.f;
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) l += exch[w * kWideQueries + q];
+          if (q < nqv) m.part_ml[it.part_base + q] = make_float2(m_used[nt][i], l);
+        }
+  }
+}
+
+// the pools as [pages * kv heads][P][d] boxes of one page and head
+struct KvMaps {
+  CUtensorMap k, v;
+};
+
+template <typename T, int D, bool WIDE>
 static cudaError_t launch_a8(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_scale,
                              const uint8_t* v_scale, const uint32_t* mask_words, uint32_t* status,
-                             const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
-  using C = a8::Cfg<D, NT, sizeof(T) == 4>;
-  const int n = NT == 1 ? p.num_dec_items : p.num_wide_items;
+                             const KvMaps& maps, cudaStream_t s) {
+  const int n = WIDE ? p.num_wide_items : p.num_dec_items;
   if (n == 0) return cudaSuccess;
+  constexpr bool SPLIT = sizeof(T) == 4;
+  constexpr int smem = WIDE ? a8::WideCfg<D, SPLIT>::SMEM : a8::NarrowCfg<D, SPLIT>::SMEM;
+  static_assert(smem + 1024 <= 227 * 1024 / 2, "two CTAs per SM at least");
+  auto kernel = WIDE ? attend_kv8_wide_kernel<T, D> : attend_kv8_kernel<T, D>;
   static std::atomic<uint64_t> configured{0};  // per instantiation and device
-  cudaError_t e = set_smem_limit(attend_kv8_kernel<T, D, NT>, C::SMEM, configured);
+  cudaError_t e = set_smem_limit(kernel, smem, configured);
   if (e != cudaSuccess) return e;
   DevMeta m = p.dev;
   test_wait_hook(&m.test_stall, &m.test_wait_us);
-  const int per_sm = std::max(1, std::min(C::MIN_CTAS, 227 * 1024 / (C::SMEM + 1024)));
+  const int per_sm = std::min(3, 227 * 1024 / (smem + 1024));
   const int grid = std::min(n, per_sm * std::max(1, p.dev.num_sms));
-  return launch_dependent(attend_kv8_kernel<T, D, NT>, dim3(grid), dim3(a8::THREADS), C::SMEM, s,
-                          true, m, p.desc.num_q_heads, p.desc.num_kv_heads, p.G, p.desc.page_size,
-                          p.desc.sm_scale * a8::kLog2e, static_cast<const T*>(q_rot), k_scale,
-                          v_scale, mask_words, NT == 1 ? m.dec_items : m.wide_items, n,
-                          m.dec_work + (NT == 1 ? 0 : 2), status, km, vm);
+  return launch_dependent(kernel, dim3(grid), dim3(a8::THREADS), smem, s, true, m,
+                          p.desc.num_q_heads, p.desc.num_kv_heads, p.G, p.desc.page_size,
+                          p.desc.sm_scale * a8::kLog2e, static_cast<const T*>(q_rot), k_scale, v_scale,
+                          mask_words, WIDE ? m.wide_items : m.dec_items, n,
+                          m.dec_work + (WIDE ? 2 : 0), status, maps.k, maps.v);
 }
 
 template <typename T, int D>
-static cudaError_t launch_a8_all(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_scale,
-                                 const uint8_t* v_scale, const uint32_t* mask_words,
-                                 uint32_t* status, const CUtensorMap& km, const CUtensorMap& vm,
-                                 cudaStream_t s) {
-  cudaError_t e = launch_a8<T, D, 1>(p, q_rot, k_scale, v_scale, mask_words, status, km, vm, s);
+static cudaError_t launch_a8_both(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_scale,
+                                  const uint8_t* v_scale, const uint32_t* mask_words,
+                                  uint32_t* status, const KvMaps& maps, cudaStream_t s) {
+  cudaError_t e = launch_a8<T, D, false>(p, q_rot, k_scale, v_scale, mask_words, status, maps, s);
   if (e == cudaSuccess)
-    e = launch_a8<T, D, 4>(p, q_rot, k_scale, v_scale, mask_words, status, km, vm, s);
+    e = launch_a8<T, D, true>(p, q_rot, k_scale, v_scale, mask_words, status, maps, s);
   return e;
 }
 
@@ -689,19 +1015,19 @@ cudaError_t launch_attend_kv8(const pie_fwd_plan_t& p, const void* q_rot, const 
                               const uint8_t* v_scale, const uint32_t* mask_words,
                               uint32_t* status, cudaStream_t s) {
   const int D = p.desc.head_dim, P = p.desc.page_size;
-  CUtensorMap km, vm;
+  KvMaps maps;
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(P),
                               cuuint64_t(p.dev.num_pool_pages) * p.desc.num_kv_heads};
   const cuuint64_t str[2] = {cuuint64_t(D), cuuint64_t(D) * P};
   const cuuint32_t box[3] = {cuuint32_t(D), cuuint32_t(P), 1};
   const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (!tc::make_map(&km, k_pool, 3, dims, str, box, sw, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
-      !tc::make_map(&vm, v_pool, 3, dims, str, box, sw, CU_TENSOR_MAP_DATA_TYPE_UINT8))
+  if (!tc::make_map(&maps.k, k_pool, 3, dims, str, box, sw, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+      !tc::make_map(&maps.v, v_pool, 3, dims, str, box, sw, CU_TENSOR_MAP_DATA_TYPE_UINT8))
     return cudaErrorInvalidValue;
   const bool bf = p.desc.dtype == PIE_BF16;
-  auto f = D == 128 ? (bf ? launch_a8_all<__nv_bfloat16, 128> : launch_a8_all<float, 128>)
-                    : (bf ? launch_a8_all<__nv_bfloat16, 64> : launch_a8_all<float, 64>);
-  return f(p, q_rot, k_scale, v_scale, mask_words, status, km, vm, s);
+  auto f = D == 128 ? (bf ? launch_a8_both<__nv_bfloat16, 128> : launch_a8_both<float, 128>)
+                    : (bf ? launch_a8_both<__nv_bfloat16, 64> : launch_a8_both<float, 64>);
+  return f(p, q_rot, k_scale, v_scale, mask_words, status, maps, s);
 }
 
 }  // namespace pie

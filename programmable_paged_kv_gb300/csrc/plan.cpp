@@ -142,6 +142,10 @@ static int choose_chunk(int64_t total_slots_x_heads) {
 // tensor-core kernel (bf16 only).
 constexpr int kTcMinQueries = 16;
 
+// 8-bit caches: lanes with more query vectors per kv head than this use the
+// tensor-core kernel (bf16, d 128); up to it, items of kWideQueries.
+constexpr int kTc8MinQueries = 32;
+
 // Multiprocessors of the current device, looked up once per device; the
 // default when no device is visible (planning on a host without a GPU).
 int device_sm_count() {
@@ -403,7 +407,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   // split-KV kernel.
   auto lane_tc = [&](int l) {
     const int n = M.row_indptr[l + 1] - M.row_indptr[l];
-    if (H.kv8) return tc8_ok && n * G > 8;
+    if (H.kv8) return tc8_ok && n * G > kTc8MinQueries;
     return tc_ok && n > 0 && (n * G >= kTcMinQueries || (H.has_mask && !mma_ok));
   };
   auto lane_list = [&](int l) { return !H.kv8 && H.has_mask && (lane_tc(l) || mma_ok); };
