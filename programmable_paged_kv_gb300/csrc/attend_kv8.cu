@@ -140,13 +140,15 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int z,
 // a lane each.  Every warp of the CTA walks the same ones.
 struct Stages {
   const uint32_t* words;
-  const int64_t* wind;
-  int row0, nrows, kb, ke, n, base;
+  int64_t row_words;  // where this lane's row's words begin
+  int nrows, kb, ke, n, base;
   uint32_t bits;
   __device__ __forceinline__ Stages(const DevMeta& m, const uint32_t* mask_words, const DecItem& it)
-      : words(mask_words), wind(m.mask_word_indptr), row0(it.row0), nrows(it.nrows),
-        kb(it.kv_begin), ke(it.kv_end), base(-1), bits(~0u) {
+      : words(mask_words), row_words(0), nrows(it.nrows), kb(it.kv_begin), ke(it.kv_end), base(-1),
+        bits(~0u) {
     n = ke > kb ? (ke - kb + kStageSlots - 1) / kStageSlots : 0;
+    const int lane = threadIdx.x & 31;  // (an item has at most kWideQueries rows)
+    if (words && lane < nrows) row_words = m.mask_word_indptr[it.row0 + lane];
   }
   // the first stage from s on that is seen, or n
   __device__ __forceinline__ int from(int s) {
@@ -155,17 +157,17 @@ struct Stages {
       if (base < 0 || s >= base + 32) {
         base = s;
         const int sb = kb + (s + int(threadIdx.x & 31)) * kStageSlots;
-        bool seen = false;
-        if (sb < ke)
-          for (int r = 0; r < nrows && !seen; ++r) {
-            const uint32_t* w = words + wind[row0 + r] + (sb >> 5);
-#pragma unroll
-            for (int i = 0; i < kStageSlots / 32; ++i) {
-              const int left = ke - sb - 32 * i;
-              if (left > 0) seen = seen || (w[i] & (left < 32 ? (1u << left) - 1u : ~0u)) != 0;
-            }
-          }
-        bits = __ballot_sync(0xffffffffu, seen);
+        const int left0 = ke - sb, left1 = left0 - 32;
+        const uint32_t use0 = left0 >= 32 ? ~0u : left0 > 0 ? (1u << left0) - 1u : 0u;
+        const uint32_t use1 = left1 >= 32 ? ~0u : left1 > 0 ? (1u << left1) - 1u : 0u;
+        uint32_t seen = 0u;
+#pragma unroll 4
+        for (int r = 0; r < nrows; ++r) {
+          const uint32_t* w = words + __shfl_sync(0xffffffffu, row_words, r) + (sb >> 5);
+          if (use0) seen |= w[0] & use0;
+          if (use1) seen |= w[1] & use1;
+        }
+        bits = __ballot_sync(0xffffffffu, seen != 0u);
       }
       const uint32_t rest = bits >> (s - base);
       if (rest) return s + __ffs(rest) - 1;
@@ -748,6 +750,14 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
     load_queries<T, D, kWideQueries, C>(S, m, it, q_rot, Hq, G, scale_log2);
     sync_compute();
     const Common all(S.lim, nqv);
+    // lane v: the mask words of query vector v's row, and of these the one over this
+    // warp's slots, fetched a stage ahead
+    const uint32_t* my_words =
+        mask_words && lane < nqv ? mask_words + m.mask_word_indptr[it.row0 + lane / G] : nullptr;
+    auto word_of = [&](int s) -> uint32_t {
+      const int p = it.kv_begin + s * kStageSlots + unit;
+      return my_words && p < it.kv_end ? my_words[p >> 5] >> (p & 31) : 0u;
+    };
     float o[NT][CH][4];
     float m_used[NT][2], l_part[NT][2];
 #pragma unroll
@@ -758,8 +768,13 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
       l_part[nt][0] = l_part[nt][1] = 0.f;
     }
 
-    for (int s = st_it.from(0); s < st_it.n; s = st_it.from(s + 1), ++gs) {
+    int s = st_it.from(0), s_next = 0;
+    uint32_t word_next = word_of(s);
+    for (; s < st_it.n; s = s_next, ++gs) {
       const int st = gs % STAGES;
+      const uint32_t my_word = word_next;
+      s_next = st_it.from(s + 1);
+      word_next = word_of(s_next);
       const int base = it.kv_begin + s * kStageSlots + unit;  // this warp's first position
       const int nvalid = max(0, min(kWarpSlots, it.kv_end - base));
       if (!dead && !mbar_wait_ns(&S.full[gs % C::BARS], (gs / C::BARS) & 1, wait_ns)) {
@@ -797,9 +812,7 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int qv = nt * 8 + 2 * t + i, lim = S.lim[qv];
-            uint32_t word = 0u;
-            if (mask_words && qv < nqv && nvalid > 0)
-              word = mask_words[m.mask_word_indptr[it.row0 + qv / G] + (base >> 5)] >> (base & 31);
+            const uint32_t word = __shfl_sync(0xffffffffu, my_word, qv);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int cs = g + 8 * j;

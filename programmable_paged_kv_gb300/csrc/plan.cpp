@@ -431,7 +431,43 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
     }
     work += slots * Hkv;
   }
-  const int CH = choose_chunk(work);
+  int CH = choose_chunk(work);
+  // 8-bit caches and windows: where that gives less than about four waves of the
+  // three CTAs per SM, the chunk that makes the waves' time shortest, an item costing
+  // its slots and about kItemSlots more (its first copies, its partials).
+  if (H.kv8 || H.window > 0) {
+    const int kItemSlots = 192;
+    static thread_local std::vector<int32_t> exts;
+    exts.clear();
+    int longest = 1;
+    for (int l = 0; l < L; ++l) {
+      if (lane_tc(l)) continue;
+      const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1];
+      const int rows = lane_wide(l) ? wide_rows : rows_per_item;
+      for (int b0 = r0; b0 < r1; b0 += rows) {
+        int skip;
+        exts.push_back(reads(l, b0, std::min(r1, b0 + rows), &skip));
+        longest = std::max(longest, exts.back());
+      }
+    }
+    const int64_t cap = 3 * static_cast<int64_t>(H.sms);
+    auto count = [&](int64_t ch) {
+      int64_t items = 0;
+      for (const int32_t e : exts) items += (e + ch - 1) / ch;
+      return items * Hkv;
+    };
+    if (count(CH) <= 4 * cap) {
+      double best = -1.0;
+      for (int n = 1; n <= 256 && (n == 1 || longest / n >= 128); n += 1 + n / 8) {
+        const int64_t ch = ((longest + n - 1) / n + kTcTileSlots - 1) / kTcTileSlots * kTcTileSlots;
+        const int64_t items = count(ch);
+        if (items == 0 || items > 4 * cap) break;
+        const double mean = static_cast<double>(work) / items + kItemSlots;
+        const double cost = static_cast<double>((items + cap - 1) / cap) * mean;
+        if (best < 0.0 || cost < best) best = cost, CH = static_cast<int>(ch);
+      }
+    }
+  }
   // tensor-core items: two query tiles per item when some lane has more than
   // 128 query vectors per kv head (they then share every K/V tile)
   int max_tc_q = 0;
