@@ -304,3 +304,203 @@ def test_pass_on_the_8_bit_cache():
         assert np.all(np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol))
         assert np.all(np.abs(outs[0][2].double().cpu().numpy() - wl) <= ltol)
         length += n
+
+
+def _state(seed, desc, lanes, **kw):
+    """Device state of one pass: pass, pages, queries, pools and scales."""
+    from programmable_paged_kv_gb300 import runner
+    p, pages = CC.make_pass(seed, desc, lanes, **kw)
+    (kc, ks), (vc, vs) = CC.pool8(seed + 1, pages, desc), CC.pool8(seed + 2, pages, desc)
+    q, k, v = (runner.to_device(x, desc.dtype) for x in (p.q, p.k, p.v))
+    return p, pages, (q, k, v), [CC.to_dev(x) for x in (kc, vc, ks, vs)]
+
+
+def test_captured_pass_replays_on_changed_inputs():
+    """append, attend and fold of one pass captured once (decode, wide and
+    tensor-core items in one plan) and replayed on other inputs: the same bits as
+    eager calls on them."""
+    desc = W.Desc(8, 2, 128, 16, W.BF16)
+    p, pages, (q, k, v), pool = _state(60, desc, [CC.tail(300, 1), CC.tail(90, 5), CC.tail(200, 20)],
+                                       fold=[W.FOLD_ALL] * 3)
+    plan = CC.plan_of(desc, p, pages, kv="e4m3")
+    q_rot, out = torch.empty_like(q), torch.empty_like(q)
+    lse = torch.empty(out.shape[:2], device="cuda")
+    frozen = CC.to_dev(np.array([299, 85, 180], np.int32))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream()
+
+    def run():
+        plan.append_kv8(q, k, v, q_rot, *pool, frozen, status, stream=stream)
+        plan.attend_kv8(q_rot, *pool, None, None, None, out, lse, status, stream=stream)
+        plan.fold(frozen, status=status, stream=stream)
+
+    start = [x.clone() for x in (*pool, frozen)]
+    torch.cuda.synchronize()
+    run()  # (first calls set the kernels' attributes)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        run()
+    for i in range(3):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(i)
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=gen, device="cuda") * (1 + 3 * i))
+        res = []
+        for replay in (True, False):
+            for x, x0 in zip((*pool, frozen), start):
+                x.copy_(x0)
+            torch.cuda.synchronize()
+            graph.replay() if replay else run()
+            torch.cuda.synchronize()
+            res.append([x.clone() for x in (q_rot, out, lse, *pool, frozen, status)])
+        assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert int(status.item()) == 0
+    plan.close()
+
+
+def test_plans_on_two_streams_at_once():
+    """Two passes with workspaces of their own, attending at the same time over
+    and over: each its own result."""
+    desc = W.Desc(8, 2, 128, 16, W.BF16)
+    runs = []
+    for i, lanes in enumerate(([CC.tail(900, 1)] * 6, [CC.tail(500, 6), CC.tail(700, 40)])):
+        p, pages, (q, _, _), pool = _state(70 + 10 * i, desc, lanes)
+        plan = CC.plan_of(desc, p, pages, kv="e4m3")
+        outs = [torch.empty_like(q) for _ in range(8)]
+        runs.append((plan, q, pool, outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(8):
+        for plan, q, pool, outs, stream in runs:
+            plan.attend_kv8(q, *pool, out_all=outs[i], stream=stream)
+    torch.cuda.synchronize()
+    for plan, q, pool, outs, _ in runs:
+        assert all(torch.equal(o, outs[0]) for o in outs[1:])
+        plan.close()
+    assert not torch.equal(runs[0][3][0][0], runs[1][3][0][0])
+
+
+def test_pool_beyond_32_bit_offsets():
+    """Pages past byte 2^32 of their pool: written and read."""
+    desc = W.Desc(8, 8, 128, 32, W.BF16)
+    lanes = [CC.tail(70, 1), CC.tail(40, 9)]
+    p, _ = CC.make_pass(80, desc, lanes)
+    pages = 140000  # 32 KB each
+    p.page_ids = (np.arange(len(p.page_ids)) * 37 % 900 + pages - 900).astype(np.int32)
+    pool = [torch.empty((pages, 8, 32, 128), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scale = [torch.empty((pages, 8), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    small = [CC.pool8(81 + i, 900, desc) for i in range(2)]
+    for t, s, (c, e) in zip(pool, scale, small):
+        t[pages - 900:].copy_(CC.to_dev(c))
+        s[pages - 900:].copy_(CC.to_dev(e))
+    from programmable_paged_kv_gb300 import runner
+    q, k, v = (runner.to_device(x, 1) for x in (p.q, p.k, p.v))
+    plan = CC.plan_of(desc, p, pages, kv="e4m3")
+    q_rot, out = torch.empty_like(q), torch.empty_like(q)
+    plan.append_kv8(q, k, v, q_rot, *pool, *scale, CC.to_dev(np.array([69, 31], np.int32)))
+    plan.attend_kv8(q_rot, *pool, *scale, out_all=out)
+    torch.cuda.synchronize()
+    local = W.Pass(**{f: getattr(p, f) for f in p.__dataclass_fields__})
+    local.page_ids = p.page_ids - (pages - 900)
+    host = [small[0][0], small[1][0], small[0][1], small[1][1]]
+    O8.append(desc, local, O8.rope(CC.values(p.k, 1), p.positions, desc.rope_base), host[0], host[2], [69, 31])
+    O8.append(desc, local, CC.values(p.v, 1), host[1], host[3], [69, 31])
+    for t, h in zip((*pool, *scale), host):
+        assert np.array_equal(t[pages - 900:].cpu().numpy(), h)
+    want, _, tol, _ = O8.attend(desc, local, q_rot.double().cpu().numpy(), O8.values(host[0], host[2]),
+                                O8.values(host[1], host[3]), weight_floor=2.0 ** -24,
+                                v_scale=2.0 ** (host[3].astype(np.float64) - O8.BIAS))
+    got = out.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol))
+    plan.close()
+
+
+@pytest.mark.parametrize("rows", [1, 8])
+def test_expired_wait_sets_timeout_and_the_context_stays_usable(rows):
+    """The split-KV kernels' producer stops before a stage (the library's test
+    hook; no copy is in flight): the waits run out, the status says so, the call
+    returns, and the same plan then attends as before."""
+    from programmable_paged_kv_gb300 import PIE_STATUS_TIMEOUT, abi
+    lib = abi.load()
+    desc = W.Desc(8, 2, 128, 16, W.BF16)
+    p, pages, (q, _, _), pool = _state(90, desc, [CC.tail(1200, rows)] * 5)
+    plan = CC.plan_of(desc, p, pages, kv="e4m3")
+    out, again = torch.empty_like(q), torch.empty_like(q)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plan.attend_kv8(q, *pool, out_all=out, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert lib.pie_fwd_test_wait_expiry(1, 300) == abi.PIE_OK
+    try:
+        plan.attend_kv8(q, *pool, out_all=again, status=status)
+        torch.cuda.synchronize()
+    finally:
+        assert lib.pie_fwd_test_wait_expiry(-1, 0) == abi.PIE_OK
+    assert int(status.item()) & PIE_STATUS_TIMEOUT
+    status.zero_()
+    plan.attend_kv8(q, *pool, out_all=again, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and torch.equal(out, again)
+    plan.close()
+
+
+def test_refused_calls():
+    """Tensors of the wrong shape, type or place, and calls for the other kind of
+    cache: refused before anything is launched."""
+    import programmable_paged_kv_gb300 as pk
+    desc = W.Desc(8, 2, 64, 16, W.BF16)
+    p, pages, (q, k, v), pool = _state(95, desc, [CC.tail(40, 2)])
+    frozen = CC.to_dev(np.array([38], np.int32))
+    plan = CC.plan_of(desc, p, pages, kv="e4m3")
+    q_rot, out = torch.empty_like(q), torch.empty_like(q)
+    good = dict(q=q, k=k, v=v, q_rot=q_rot, k_pool=pool[0], v_pool=pool[1], k_scale=pool[2],
+                v_scale=pool[3], frozen_len=frozen)
+    for name, bad in (("q", q.float()), ("q", q[:1]), ("k", k.transpose(1, 2)), ("v", v.cpu()),
+                      ("q_rot", q_rot.half()), ("k_pool", pool[0].int()), ("k_pool", pool[0][:-1]),
+                      ("v_pool", pool[1].transpose(2, 3).contiguous().transpose(2, 3)),
+                      ("k_scale", pool[2][:, :1]), ("v_scale", pool[3].float()),
+                      ("frozen_len", frozen.long())):
+        with pytest.raises(ValueError):
+            plan.append_kv8(**{**good, name: bad})
+    att = dict(q_rot=q, k_pool=pool[0], v_pool=pool[1], k_scale=pool[2], v_scale=pool[3], out_all=out)
+    for name, bad in (("q_rot", q[..., :32]), ("out_all", out.float()), ("k_pool", pool[0].cpu()),
+                      ("lse_all", torch.empty((2, 8), device="cuda", dtype=torch.float64)),
+                      ("out_readout", out)):
+        with pytest.raises(ValueError):
+            plan.attend_kv8(**{**att, name: bad})
+    with pytest.raises(pk.PieError) as e:  # no mask in the plan
+        plan.attend_kv8(**att, mask_words=torch.zeros(8, dtype=torch.int32, device="cuda"))
+    assert e.value.code == pk.abi.PIE_EINVAL
+    for call in (lambda: plan.append_kv(q, k, v, q_rot, pool[0], pool[1], frozen),
+                 lambda: plan.attend(q, pool[0], pool[1], out_all=out)):
+        with pytest.raises(pk.PieError) as e:
+            call()
+        assert e.value.code == pk.abi.PIE_EINVAL
+    # a row of codes off the 16-byte boundary
+    flat = torch.empty(pool[0].numel() + 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(pk.PieError):
+        plan.attend_kv8(**{**att, "k_pool": flat[8:-8].view(pool[0].shape)})
+    plan.close()
+    plain = CC.plan_of(desc, p, pages)
+    with pytest.raises(pk.PieError) as e:
+        plain.append_kv8(**good)
+    assert e.value.code == pk.abi.PIE_EINVAL
+    plain.close()
+    none = pk.ForwardPlan(pk.make_desc(desc), pk.make_meta(p, pages))
+    with pytest.raises(ValueError):
+        none.attend_kv8(**att)
+    none.close()
+    with pytest.raises(ValueError):
+        pk.make_cache("int4")
+
+
+def test_copy_pages_refusals():
+    import programmable_paged_kv_gb300 as pk
+    pool = torch.zeros((8, 32), dtype=torch.uint8, device="cuda")
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for pools, src, dst in (([pool, pool[:4]], i, i), ([pool.t()], i, i), ([pool.cpu()], i, i),
+                            ([pool], i.long(), i), ([pool], i, i[:1]), ([pool[0, 0]], i, i)):
+        with pytest.raises(ValueError):
+            pk.copy_pages(pools, src, dst)
+    pk.copy_pages([], i, i)
+    pk.copy_pages([pool], i[:0], i[:0])
