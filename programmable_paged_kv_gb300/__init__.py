@@ -10,6 +10,7 @@ if the library is missing every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import itertools
 import types
 from typing import Optional
 
@@ -163,22 +164,21 @@ def copy_pages(pools, src, dst, status=None, stream=None) -> None:
     line = torch.Size((n_pairs,))
     src_p, dst_p = p(src, "src", line, torch.int32), p(dst, "dst", line, torch.int32)
     status_p = p(status, "status", None, 4)
-    ptrs, sizes, pages, here = [], [], -1, p.device
-    for t in pools:
-        if t.dim() == 0 or not t.is_contiguous() or t.get_device() != here:
-            raise ValueError("a pool must be a contiguous tensor of pages on the current CUDA device")
-        n = t.size(0)
-        if n != pages:
-            if pages >= 0:
-                raise ValueError("the pools must have the same number of pages")
-            pages = n
-        size = t.nbytes
-        if size:  # (a pool whose pages hold nothing has nothing to copy)
-            ptrs.append(t.data_ptr())
-            sizes.append(size // n)
+    # (a model has dozens of pools: each check one pass over all of them)
+    pools, T = list(pools), torch.Tensor
+    if not all(map(T.dim, pools)) or not all(map(T.is_contiguous, pools)) or \
+            any(d != p.device for d in map(T.get_device, pools)):
+        raise ValueError("a pool must be a contiguous tensor of pages on the current CUDA device")
+    counts = set(map(T.size, pools, itertools.repeat(0)))
+    if len(counts) > 1:
+        raise ValueError("the pools must have the same number of pages")
+    pages = counts.pop() if counts else 0
+    ptrs, sizes = list(map(T.data_ptr, pools)), [t.nbytes for t in pools]
+    if 0 in sizes:  # (a pool whose pages hold nothing has nothing to copy)
+        ptrs, sizes = [a for a, b in zip(ptrs, sizes) if b], [b for b in sizes if b]
     if not ptrs or n_pairs == 0:
         return
-    ptrs, sizes = np.array(ptrs, np.uint64), np.array(sizes, np.int64)
+    ptrs, sizes = np.array(ptrs, np.uint64), np.array(sizes, np.int64) // pages
     abi.check(abi.load().pie_fwd_copy_pages(ptrs.size, ptrs.ctypes.data, sizes.ctypes.data, pages,
                                             n_pairs, src_p, dst_p, status_p, p.stream),
               "pie_fwd_copy_pages")
@@ -262,13 +262,13 @@ class _Args:
 
     def __init__(self, stream):
         import torch
-        here = torch.cuda.current_stream()
-        self.device = here.device_index
+        self.device = torch.cuda.current_device()
         if stream is None:
-            stream = here
-        elif stream.device_index != self.device:
+            self.stream = torch._C._cuda_getCurrentRawStream(self.device)
+        elif stream.device_index == self.device:
+            self.stream = stream.cuda_stream
+        else:
             raise ValueError("the stream must belong to the current CUDA device")
-        self.stream = stream.cuda_stream
 
     def __call__(self, t, what: str, shape=None, dtype=None):
         if t is None:

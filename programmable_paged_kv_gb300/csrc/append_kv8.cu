@@ -9,7 +9,7 @@
 // scale grows shifts its codes' exponents (only values that fall under e4m3's
 // smallest normal lose bits).  A page's codes are read only then.
 // Three kinds of CTAs per page, 8 warps each: K (a warp per kv head, which holds
-// the head's rows of the page in registers between finding the scale and writing
+// the head's rows of the page in registers while it finds the scale and then writes
 // the codes; the rows' rotation angles are shared), V (the same without a
 // rotation), and the rows' query heads.  All global accesses are 16-byte vectors
 // of a row, a warp's worth of rows in flight at once.
@@ -165,18 +165,22 @@ __device__ __forceinline__ void regrow(uint8_t* rows, uint32_t keep, int old, in
   }
 }
 
-// One head's rows of a page, from the floats `x` that lane (row, c) holds of row
-// i = it * RPI + lane / (32 / RPI): find the exponent, move the live codes, write
-// `put(it, exponent)` for every row that is written.
-template <int D, int ITS, int RPI, int N, typename Put>
-__device__ __forceinline__ void quantise(float (&x)[ITS][N], const bool (&mine)[ITS], uint8_t* codes,
-                                         uint8_t* scale, uint32_t keep, int lane, Put put) {
+// One head's rows of a page, ITS steps of them per lane: `value(it, x)` gives the N
+// elements this lane holds of step it's row (from registers; called twice, which
+// costs less than keeping the results would in resident warps).  Finds the exponent,
+// moves the live codes, and lets `put(it, x)` write the scaled elements.
+template <int D, int ITS, int N, typename Value, typename Put>
+__device__ __forceinline__ void quantise(const bool (&mine)[ITS], uint8_t* codes, uint8_t* scale,
+                                         uint32_t keep, int lane, Value value, Put put) {
   float amax = 0.f;
 #pragma unroll
   for (int it = 0; it < ITS; ++it)
-    if (mine[it])
+    if (mine[it]) {
+      float x[N];
+      value(it, x);
 #pragma unroll
-      for (int e = 0; e < N; ++e) amax = fmaxf(amax, fabsf(x[it][e]));
+      for (int e = 0; e < N; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    }
   const int old = int(*scale) - fp8::kBias;
   int ex = needed_exp(warp_max(amax));
   if (keep) {
@@ -188,9 +192,11 @@ __device__ __forceinline__ void quantise(float (&x)[ITS][N], const bool (&mine)[
 #pragma unroll
   for (int it = 0; it < ITS; ++it)
     if (mine[it]) {
+      float x[N];
+      value(it, x);
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[it][e] = fp8::scale2(x[it][e], -ex);
-      put(it);
+      for (int e = 0; e < N; ++e) x[e] = fp8::scale2(x[e], -ex);
+      put(it, x);
     }
 }
 
@@ -198,7 +204,7 @@ __device__ __forceinline__ void quantise(float (&x)[ITS][N], const bool (&mine)[
 
 // MAXR: the most rows one page holds (16 or 32).
 template <typename T, int D, int MAXR>
-__global__ void __launch_bounds__(ak::THREADS) append_kv8_kernel(
+__global__ void __launch_bounds__(ak::THREADS, sizeof(T) * MAXR <= 32 ? 3 : sizeof(T) * MAXR <= 64 ? 2 : 1) append_kv8_kernel(
     DevMeta m, int Hq, int Hkv, int P, int head_ctas, const T* q, const T* k, const T* v, T* q_rot,
     uint8_t* k_pool, uint8_t* v_pool, uint8_t* k_scale, uint8_t* v_scale,
     const int32_t* frozen_len, uint32_t* status) {
@@ -208,6 +214,7 @@ __global__ void __launch_bounds__(ak::THREADS) append_kv8_kernel(
   constexpr int UL = H / VEC;          // lanes per rotated row: c holds elements c VEC .. of both halves
   // angle e of vector c of row i: neighbouring lanes' angles side by side
   extern __shared__ Angle ang[];  // [rows][VEC][UL]
+  __shared__ uint8_t offs[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WriteBlock wb = m.wblocks[blockIdx.x];
   const int32_t* rows = m.wrow + wb.row0;
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(ak::THREADS) append_kv8_kernel(
   const int ang0 = is_k ? 0 : unit0 / Hq, ang1 = is_k ? wb.nrows : is_v ? 0 : (unit0 + units - 1) / Hq + 1;
   for (int j = threadIdx.x; j < (ang1 - ang0) * H; j += THREADS) {
     const int i = j / H, f = j % H;
-    const uint64_t turns = uint64_t(uint32_t(m.positions[rows[ang0 + i]])) * m.rope_turn[f];
+    const uint64_t turns = uint64_t(uint32_t(m.wpos[wb.row0 + ang0 + i])) * m.rope_turn[f];
     Angle& a = ang[i * H + (f % VEC) * UL + f / VEC];
     if (is_k) {
       a = angle(turns);
@@ -235,6 +242,9 @@ __global__ void __launch_bounds__(ak::THREADS) append_kv8_kernel(
       a.sh = s;
     }
   }
+  // the i-th row's slot offset: the i-th set bit
+  if (threadIdx.x < 32 && ((wb.written >> threadIdx.x) & 1u))
+    offs[__popc(wb.written & ((1u << threadIdx.x) - 1u))] = uint8_t(threadIdx.x);
   const int slot0 = wb.lpage * P;
   const int kv_len = m.kv_len[wb.lane];
   grid_dep_wait();
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(ak::THREADS) append_kv8_kernel(
 
   const int frozen = frozen_len[wb.lane];
   if (part == 0 && threadIdx.x < wb.nrows) {
-    const int r = rows[threadIdx.x], slot = m.slots[r];
+    const int r = rows[threadIdx.x], slot = slot0 + offs[threadIdx.x];
     if (slot < frozen) set_status(status, PIE_STATUS_FROZEN_WRITE);
     if (r == m.row_indptr[wb.lane] && m.fold_mode[wb.lane] != PIE_FOLD_NONE && slot != frozen)
       set_status(status, PIE_STATUS_FOLD_GAP);
@@ -283,61 +293,59 @@ __global__ void __launch_bounds__(ak::THREADS) append_kv8_kernel(
     constexpr int RPI = 32 / UL, ITS = MAXR / RPI;  // rows per step, steps
     const int c = lane % UL;
     uint8_t* codes = k_pool + cell * P * D;
-    float x[ITS][2 * VEC];  // the rotated row's low part, then its high part
     bool mine[ITS];
     int off[ITS];
     uint4 raw[ITS][2];
 #pragma unroll
     for (int it = 0; it < ITS; ++it) {
       const int i = it * RPI + lane / UL;
-      const int r = i < wb.nrows ? rows[i] : rows[0];
-      const int slot = m.slots[r];
-      off[it] = slot - slot0;
-      mine[it] = i < wb.nrows && slot >= frozen;
+      mine[it] = i < wb.nrows;
+      off[it] = mine[it] ? offs[i] : 0;
+      mine[it] = mine[it] && slot0 + off[it] >= frozen;
       if (mine[it]) {
-        const T* src = k + (int64_t(r) * Hkv + g) * D + c * VEC;
+        const T* src = k + (int64_t(rows[i]) * Hkv + g) * D + c * VEC;
         raw[it][0] = *reinterpret_cast<const uint4*>(src);
         raw[it][1] = *reinterpret_cast<const uint4*>(src + H);
       }
     }
+    quantise<D, ITS, 2 * VEC>(
+        mine, codes, k_scale + cell, keep, lane,
+        [&](int it, float* x) {  // the rotated row's low part, then its high part
+          const int i = it * RPI + lane / UL;
+          float a[VEC], b[VEC];
+          unpack16<T>(raw[it][0], a);
+          unpack16<T>(raw[it][1], b);
 #pragma unroll
-    for (int it = 0; it < ITS; ++it) {
-      if (!mine[it]) continue;
-      const int i = it * RPI + lane / UL;
-      float a[VEC], b[VEC];
-      unpack16<T>(raw[it][0], a);
-      unpack16<T>(raw[it][1], b);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const Angle t = ang[i * H + e * UL + c];
-        x[it][e] = rot_odd(a[e], t.ch, t.cl, b[e], t.sh, t.sl);
-        x[it][VEC + e] = rot_odd(b[e], t.ch, t.cl, -a[e], t.sh, t.sl);
-      }
-    }
-    quantise<D, ITS, RPI, 2 * VEC>(x, mine, codes, k_scale + cell, keep, lane, [&](int it) {
-      store_codes<VEC>(codes + off[it] * D + c * VEC, x[it]);
-      store_codes<VEC>(codes + off[it] * D + H + c * VEC, x[it] + VEC);
-    });
+          for (int e = 0; e < VEC; ++e) {
+            const Angle t = ang[i * H + e * UL + c];
+            x[e] = rot_odd(a[e], t.ch, t.cl, b[e], t.sh, t.sl);
+            x[VEC + e] = rot_odd(b[e], t.ch, t.cl, -a[e], t.sh, t.sl);
+          }
+        },
+        [&](int it, const float* x) {
+          store_codes<VEC>(codes + off[it] * D + c * VEC, x);
+          store_codes<VEC>(codes + off[it] * D + H + c * VEC, x + VEC);
+        });
   } else {
     constexpr int VLN = D / VEC, RPI = 32 / VLN, ITS = MAXR / RPI;
     const int c = lane % VLN;
     uint8_t* codes = v_pool + cell * P * D;
-    float x[ITS][VEC];
     bool mine[ITS];
     int off[ITS];
+    uint4 raw[ITS];
 #pragma unroll
     for (int it = 0; it < ITS; ++it) {
       const int i = it * RPI + lane / VLN;
-      const int r = i < wb.nrows ? rows[i] : rows[0];
-      const int slot = m.slots[r];
-      off[it] = slot - slot0;
-      mine[it] = i < wb.nrows && slot >= frozen;
+      mine[it] = i < wb.nrows;
+      off[it] = mine[it] ? offs[i] : 0;
+      mine[it] = mine[it] && slot0 + off[it] >= frozen;
       if (mine[it])
-        unpack16<T>(*reinterpret_cast<const uint4*>(v + (int64_t(r) * Hkv + g) * D + c * VEC), x[it]);
+        raw[it] = *reinterpret_cast<const uint4*>(v + (int64_t(rows[i]) * Hkv + g) * D + c * VEC);
     }
-    quantise<D, ITS, RPI, VEC>(x, mine, codes, v_scale + cell, keep, lane, [&](int it) {
-      store_codes<VEC>(codes + off[it] * D + c * VEC, x[it]);
-    });
+    quantise<D, ITS, VEC>(
+        mine, codes, v_scale + cell, keep, lane,
+        [&](int it, float* x) { unpack16<T>(raw[it], x); },
+        [&](int it, const float* x) { store_codes<VEC>(codes + off[it] * D + c * VEC, x); });
   }
 }
 

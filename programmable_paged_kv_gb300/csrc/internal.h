@@ -48,8 +48,8 @@ __host__ __device__ inline int window_pages(int block) { return block < -1 ? -1 
 
 // A page that rows of the pass write in a cache of 8-bit codes: the rows
 // wrow[row0 .. row0 + nrows) of `lane`, all in its page-table entry `lpage`,
-// whose physical page is `page`; bit o of `written` says a row writes slot
-// offset o.
+// whose physical page is `page`, by rising slot; bit o of `written` says a row
+// writes slot offset o (so the i-th row writes at the i-th set bit).
 struct alignas(16) WriteBlock {
   int32_t lane, lpage, page, row0;
   int32_t nrows;
@@ -147,7 +147,8 @@ struct DevMeta {
   const float* rope_freq;           // [d/2]
   const uint64_t* rope_turn;        // [d/2] turns per position, 0.64 fixed point (8-bit caches)
   const WriteBlock* wblocks;        // pages written (8-bit caches)
-  const int32_t* wrow;              // [N] rows in the order of the pages they write
+  const int32_t* wrow;              // [N] rows in the order of the slots they write
+  const int32_t* wpos;              // [N] their positions
   const DecItem* wide_items;        // 8-bit caches: items of up to kWideQueries query vectors
   const DecItem* dec_items;
   const TcItem* tc_items;

@@ -98,7 +98,7 @@ struct HostPlan {
   int window = 0, sinks = 0, sink_pages = 0;
   std::vector<uint64_t> rope_turn;
   std::vector<WriteBlock> wblocks;
-  std::vector<int32_t> wrow;
+  std::vector<int32_t> wrow, wpos;
   std::vector<DecItem> wide;
   bool has_mask = false, any_channel = false;
   bool dec_lists = false;  // some split-KV item walks a compacted list
@@ -191,6 +191,8 @@ static int build_write_blocks(const pie_fwd_desc& D, const pie_fwd_meta& M, Host
       H.wblocks.push_back(b);
     }
   }
+  H.wpos.resize(H.N);
+  for (int i = 0; i < H.N; ++i) H.wpos[i] = M.positions[H.wrow[i]];
   static thread_local std::vector<int32_t> pages;
   pages.clear();
   for (const WriteBlock& b : H.wblocks) pages.push_back(b.page);
@@ -345,6 +347,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
 
   H.wblocks.clear();
   H.wrow.clear();
+  H.wpos.clear();
   H.rope_turn.clear();
   if (H.kv8) {
     // turns per position, base^(-2i/d) / (2 pi), whole turns dropped
@@ -658,7 +661,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
 struct Layout {
   size_t row_indptr, positions, slots, kv_len, page_indptr, page_ids, fold_mode, fold_count,
       row_lane, mask_word_indptr, readout, ro_indptr, ro_idx, rope_freq, dec, tc, comb, mblocks,
-      row_block, rope_turn, wblocks, wrow, wide;
+      row_block, rope_turn, wblocks, wrow, wpos, wide;
   size_t copy_bytes;  // everything above
   size_t part_o, part_ml, list, lrow, cmask, list_len, list_mode, mask_tiles, dec_work;
   size_t total;
@@ -696,6 +699,7 @@ static Layout make_layout(const pie_fwd_desc& D, const HostPlan& H) {
   Y.rope_turn = take(sizeof(uint64_t) * H.rope_turn.size());
   Y.wblocks = take(sizeof(WriteBlock) * H.wblocks.size());
   Y.wrow = take(sizeof(int32_t) * H.wrow.size());
+  Y.wpos = take(sizeof(int32_t) * H.wpos.size());
   Y.wide = take(sizeof(DecItem) * H.wide.size());
   // the split-KV kernel's work counter and finished-CTA count (zero from the
   // upload; the kernel sets them back to zero when it ends)
@@ -829,6 +833,7 @@ int pie_fwd_cache_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   put(Y.rope_turn, H.rope_turn.data(), sizeof(uint64_t) * H.rope_turn.size());
   put(Y.wblocks, H.wblocks.data(), sizeof(WriteBlock) * H.wblocks.size());
   put(Y.wrow, H.wrow.data(), sizeof(int32_t) * H.wrow.size());
+  put(Y.wpos, H.wpos.data(), sizeof(int32_t) * H.wpos.size());
   put(Y.wide, H.wide.data(), sizeof(DecItem) * H.wide.size());
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -905,6 +910,7 @@ int pie_fwd_cache_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   dm.rope_turn = reinterpret_cast<const uint64_t*>(w + Y.rope_turn);
   dm.wblocks = reinterpret_cast<const WriteBlock*>(w + Y.wblocks);
   dm.wrow = reinterpret_cast<const int32_t*>(w + Y.wrow);
+  dm.wpos = reinterpret_cast<const int32_t*>(w + Y.wpos);
   dm.wide_items = reinterpret_cast<const DecItem*>(w + Y.wide);
   dm.window = H.window;
   dm.sinks = H.sinks;
