@@ -65,13 +65,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Geometry of a kernel for items of NQ query vectors whose warps come to a stage in
 // groups of READERS.
-template <int D, int NQ, int READERS, bool SPLIT>
+template <int D, int NQ, int READERS, int RING, bool SPLIT>
 struct Cfg {
   static constexpr int KS = D / 16;                      // 16-wide steps of d
   static constexpr int HALF = kStageSlots * D;           // K (or V) codes of a stage
   static constexpr int STAGE = 2 * HALF;
-  // 48 KB of ring per CTA: three CTAs per SM keep 144 KB in flight
-  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int STAGES = D == 128 ? RING : 2 * RING;
   // barriers of the stages: a multiple of the groups, at least the ring's, so that
   // each belongs to one group, which then sees every phase of it (copies may
   // complete in any order)
@@ -419,11 +418,13 @@ __device__ __forceinline__ void zero_rows(uint8_t* v, int first, int n) {
 // items of up to 8 query vectors
 // ---------------------------------------------------------------------------
 namespace a8 {
+// A ring of 64 KB: the warps hold two of four stages while they compute, so three
+// CTAs per SM keep 96 KB on their way (with 48 KB it was 48, and the decode batch 60
+// us).  The warps' states are merged in the item's last stage, held back for it.
 template <int D, bool SPLIT>
-struct NarrowCfg : Cfg<D, 8, 2, SPLIT> {
-  static constexpr int OROW = D + 4;                        // (float2 stores of 4 rows on distinct banks)
-  static constexpr int MERGE = WARPS * 8 * (OROW + 2) * 4;  // the warps' states
-  static constexpr int SMEM = NarrowCfg::BASE + MERGE;
+struct NarrowCfg : Cfg<D, 8, 2, 4, SPLIT> {
+  static constexpr int SMEM = NarrowCfg::BASE + 2 * WARPS * 8 * 4;  // + maxima and sums
+  static_assert(WARPS * 8 * D * 4 <= NarrowCfg::STAGE, "the states fit the held stage");
 };
 }  // namespace a8
 
@@ -490,7 +491,9 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
 #pragma unroll
     for (int n = 0; n < KS; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
-    for (int s = st_it.from(0); s < st_it.n; s = st_it.from(s + 1), ++gs) {
+    const int gs0 = gs;
+    for (int s = st_it.from(0), next; s < st_it.n; s = next, ++gs) {
+      next = st_it.from(s + 1);
       if ((gs & 1) != pair || dead) continue;  // the other pair's stage
       const int st = gs % STAGES;
       const int base = it.kv_begin + s * kStageSlots + half;  // this warp's first position
@@ -630,15 +633,26 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
             }
         }
       }
+      // (the item's last stage stays held for the merge)
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.empty[gs % BARS]);
+      if (lane == 0 && next < st_it.n) mbar_arrive(&S.empty[gs % BARS]);
     }
 
-    // ---- merge the warps' states into the item's partials (the buffer's last
-    // readers have passed two barriers since)
-    float* mw = reinterpret_cast<float*>(S.rest);  // [WARPS][8]
-    float* lw = mw + WARPS * 8;                    // [WARPS][8]
-    float* ow = lw + WARPS * 8;                    // [WARPS][8][OROW]
+    // ---- merge the warps' states into the item's partials, in the held stage
+    // (pairs of elements XORed by the query, so that 4 rows' stores hit distinct
+    // banks)
+    if (gs == gs0) {  // no slot: empty states
+      for (int i = threadIdx.x; i < nqv * D; i += WARPS * 32) {
+        const int64_t at = int64_t(it.part_base) + i / D;
+        m.part_o[at * D + i % D] = 0.f;
+        if (i % D == 0) m.part_ml[at] = make_float2(-INFINITY, 0.f);
+      }
+      continue;
+    }
+    float* mw = reinterpret_cast<float*>(S.rest);                                   // [WARPS][8]
+    float* lw = mw + WARPS * 8;                                                     // [WARPS][8]
+    float2* ow = reinterpret_cast<float2*>(S.ring + (gs - 1) % STAGES * C::STAGE);  // [WARPS][8][D / 2]
+    sync_compute();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float l = l_part[i];
@@ -649,31 +663,38 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
         mw[warp * 8 + q] = m_used[i];
         lw[warp * 8 + q] = l;
       }
-      float* orow = ow + (warp * 8 + q) * C::OROW;
+      float2* orow = ow + (warp * 8 + q) * (D / 2);
 #pragma unroll
-      for (int n = 0; n < KS; ++n)
-        *reinterpret_cast<float2*>(orow + 16 * n + 2 * g) = make_float2(o[n][i], o[n][2 + i]);
+      for (int n = 0; n < KS; ++n) orow[(8 * n + g) ^ (t << 2)] = make_float2(o[n][i], o[n][2 + i]);
     }
     sync_compute();
-    for (int i = threadIdx.x; i < nqv * D; i += WARPS * 32) {
-      const int qq = i / D, cd = i % D;
+    for (int i = threadIdx.x; i < nqv * (D / 2); i += WARPS * 32) {
+      const int qq = i / (D / 2), c = i % (D / 2);
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mw[w * 8 + qq]);
-      float O = 0.f, Ls = 0.f;
+      float2 O = make_float2(0.f, 0.f);
+      float Ls = 0.f;
       if (M != -INFINITY) {
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
           const float mv = mw[w * 8 + qq];
           const float f = mv == -INFINITY ? 0.f : ex2(mv - M);
-          O = fmaf(f, ow[(w * 8 + qq) * C::OROW + cd], O);
+          const float2 x = ow[(w * 8 + qq) * (D / 2) + (c ^ (qq >> 1 << 2))];
+          O.x = fmaf(f, x.x, O.x);
+          O.y = fmaf(f, x.y, O.y);
           Ls = fmaf(f, lw[w * 8 + qq], Ls);
         }
       }
       const int64_t at = int64_t(it.part_base) + qq;
-      m.part_o[at * D + cd] = O;
-      if (cd == 0) m.part_ml[at] = make_float2(M, Ls);
+      reinterpret_cast<float2*>(m.part_o + at * D)[c] = O;
+      if (c == 0) m.part_ml[at] = make_float2(M, Ls);
     }
+    // the held stage back to the producer (generic writes into a buffer that the
+    // copy engine rewrites next)
+    fence_proxy_async_smem();
+    sync_compute();
+    if (((gs - 1) & 1) == pair && lane == 0 && !dead) mbar_arrive(&S.empty[(gs - 1) % BARS]);
   }
 }
 
@@ -682,7 +703,7 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
 // ---------------------------------------------------------------------------
 namespace a8 {
 template <int D, bool SPLIT>
-struct WideCfg : Cfg<D, kWideQueries, WARPS, SPLIT> {
+struct WideCfg : Cfg<D, kWideQueries, WARPS, 3, SPLIT> {
   // weights [query][slot] in fp16, rows padded by 16 bytes (ldmatrix and the
   // writers' stores hit distinct banks), and their rests for fp32
   static constexpr int PROW = kStageSlots * 2 + 16;
