@@ -238,8 +238,9 @@ __device__ __forceinline__ void produce(const Shared<C>& S, const DevMeta& m, in
       }
     }
   };
-  int ticket = 0;  // lane 0: the next item, asked for while the last one streams
-  if (lane == 0) ticket = atomicAdd(work, 1);
+  // the CTA's first item is its own number, the next ones come from the counter,
+  // asked for (by lane 0) while the last one streams
+  int ticket = blockIdx.x;
   for (int k = 0;; ++k) {
     int idx = __shfl_sync(0xffffffffu, ticket, 0);
     if (idx >= num_items) idx = -1;
@@ -253,7 +254,7 @@ __device__ __forceinline__ void produce(const Shared<C>& S, const DevMeta& m, in
       mbar_arrive(&S.item_full[q]);
     }
     if (idx < 0) break;
-    if (lane == 0) ticket = atomicAdd(work, 1);
+    if (lane == 0) ticket = int(gridDim.x) + atomicAdd(work, 1);
     const DecItem it = items[idx];
     Stages seen(m, mask_words, it);
     const int i = pi < ppt ? pi : 0;
