@@ -461,13 +461,14 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
     };
     if (count(CH) <= 4 * cap) {
       double best = -1.0;
-      for (int n = 1; n <= 256 && (n == 1 || longest / n >= 128); n += 1 + n / 8) {
-        const int64_t ch = ((longest + n - 1) / n + kTcTileSlots - 1) / kTcTileSlots * kTcTileSlots;
+      for (int64_t ch = kTcTileSlots;; ch += std::max<int64_t>(1, ch / 1024) * kTcTileSlots) {
         const int64_t items = count(ch);
-        if (items == 0 || items > 4 * cap) break;
+        if (items == 0) break;
+        if (items > 4 * cap) continue;
         const double mean = static_cast<double>(work) / items + kItemSlots;
         const double cost = static_cast<double>((items + cap - 1) / cap) * mean;
         if (best < 0.0 || cost < best) best = cost, CH = static_cast<int>(ch);
+        if (ch >= longest) break;
       }
     }
   }
