@@ -399,27 +399,32 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
     // at a time (16 lanes of 16 bytes each), their powers of two to their lanes
     int up = 0;
     {
-      const int c = lane & 15;
+      const int c = lane & 15, lg = fp8::log2i(G);
       uint4 u[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int qr = t * kTcTileQueries + quad * 32 + 2 * i + (lane >> 4);
         u[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (qr < nqv)
+        if (qr < nqv) {
+          const int r = qr >> lg, hd = qr & (G - 1);  // (G divides 128)
           u[i] = *reinterpret_cast<const uint4*>(
-              q_rot + (int64_t(it.row0 + qr / G) * Hq + it.kv_head * G + qr % G) * D + c * 8);
+              q_rot + (int64_t(it.row0 + r) * Hq + it.kv_head * G + hd) * D + c * 8);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float x[8], big = 0.f;
+        // the largest magnitude: bf16 magnitudes order as whole numbers do
+        const uint32_t m4 = __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu),
+                                     __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu));
+        uint32_t big = max(m4 & 0xFFFFu, m4 >> 16);
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, off));
+        const int ue = fp8::query_exp(__uint_as_float(big << 16));
+        const float by = fp8::pow2i(ue);
+        float x[8];
         unpack16<__nv_bfloat16>(u[i], x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-        const int ue = fp8::query_exp(big);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fp8::scale2(x[e], ue);
+        for (int e = 0; e < 8; ++e) x[e] *= by;
         const int r = quad * 32 + 2 * i + (lane >> 4);
         *reinterpret_cast<uint4*>(S.q[t][c >> 3] + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
             make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]),

@@ -76,10 +76,10 @@ struct PageBatches {
       v = v_scale[at];
     }
   }
-  __device__ __forceinline__ PageBatches(const DevMeta& m, int lane_of, int skip_, int kv_head_,
+  __device__ __forceinline__ PageBatches(const DevMeta& m, int first_page, int skip_, int kv_head_,
                                          int ke_, int tiles_, int Hkv_, int P_, const uint8_t* ks,
                                          const uint8_t* vs, TileAt at)
-      : pages(m.page_ids + m.page_indptr[lane_of]), k_scale(ks), v_scale(vs), Hkv(Hkv_),
+      : pages(m.page_ids + first_page), k_scale(ks), v_scale(vs), Hkv(Hkv_),
         kv_head(kv_head_), lp(log2i(P_)), ke(ke_), sink_pages(m.sink_pages), skip(skip_),
         num_pool_pages(m.num_pool_pages), tiles(tiles_), lppt(6 - lp), ltpb(lp - 1),
         lane(threadIdx.x & 31), tile_at(at) {

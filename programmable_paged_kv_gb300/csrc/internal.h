@@ -21,7 +21,9 @@ namespace pie {
 // chunks used come from the list's length (masked_chunks).  In windowed passes
 // kv_begin and kv_end count the slots the row block reads one after another --
 // the sink pages, then the pages from the window's first on -- and `block` is
-// -1 - (the pages left out between them); window_pages() below decodes it.
+// -1 - (the pages left out between them); window_pages() below decodes it.  In
+// passes over 8-bit caches `lane` (of a TcItem too) is where the lane's page-table
+// entries begin in page_ids: one load less before an item's first copy.
 struct alignas(16) DecItem {
   int32_t lane, kv_head, row0, nrows;
   int32_t kv_begin, kv_end, part_base, block;

@@ -575,6 +575,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
     const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1], n = r1 - r0;
     if (n == 0) continue;
     const bool use_tc = lane_tc(l);
+    const int32_t item_lane = H.kv8 ? M.page_indptr[l] : l;
     const bool wide = lane_wide(l);
     const int blk_rows = use_tc ? tc_rows : wide ? wide_rows : rows_per_item;
     const int stride = use_tc ? kTcTileQueries : wide ? kWideQueries : H.nq;
@@ -607,7 +608,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
         if (use_tc) {
           for (int c = 0; c < nchunks; ++c) {
             const int kb = c * chunk, ke = std::min(ext, kb + chunk);
-            H.tc.push_back(TcItem{l, g, b0, b1 - b0, kb, ke, static_cast<int32_t>(part),
+            H.tc.push_back(TcItem{item_lane, g, b0, b1 - b0, kb, ke, static_cast<int32_t>(part),
                                   direct ? 1 : 0, mblk, c, nchunks, skip});
             part += direct ? 0 : stride * H.tc_nt;
           }
@@ -622,7 +623,7 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
             const int kb = c * chunk;
             const int32_t pb = static_cast<int32_t>(part + int64_t(c) * stride);
             di[c] = mblk >= 0 ? DecItem{l, g, b0, b1 - b0, c, nchunks, pb, mblk}
-                              : DecItem{l, g, b0, b1 - b0, kb, std::min(ext, kb + chunk), pb, -1 - skip};
+                              : DecItem{item_lane, g, b0, b1 - b0, kb, std::min(ext, kb + chunk), pb, -1 - skip};
           }
           part += int64_t(nchunks) * stride;
         }
