@@ -21,8 +21,12 @@
 //     without error;
 //   * sine and cosine of the remaining eighth of a turn are their power series
 //     in 64-bit fixed point (error below 2^-40), kept as two floats each;
-//   * x cos - y sin is a sum of exact products (FMA residuals), rounded to odd
-//     in fp32, so that the rounding to e4m3 that follows is the only one.
+//   * x cos - y sin, where it matters, is a sum of exact products (FMA residuals),
+//     rounded to odd in fp32, so that the rounding to e4m3 that follows is the only
+//     one.  It matters where the plain fp32 rotation lies within its error of a
+//     border between two codes (or the largest magnitude of one between two
+//     exponents): about one value in 2^16.  All others keep the plain one's code
+//     (taking the exact path throughout cost 6 of 27 us on 4,096 rows).
 // Queries need no more than fp32 and take the leading floats alone.
 //
 // Bound: HBM for prompts (q, k, v in, q_rot and codes out), latency for a
@@ -115,6 +119,11 @@ __device__ __forceinline__ float rot_odd(float x, float ch, float cl, float y, f
   return __uint_as_float(u);
 }
 
+// The plain rotation is off by at most 2^-22 (|x| + |y|): a step of fp32 for the
+// angle's leading float (truncated), half a step each for the product and the FMA.
+// Twice that:
+constexpr float kRotErr = 0x1p-21f;
+
 // the smallest e in [kMinExp, kMaxExp] with amax <= 448 * 2^e
 __device__ __forceinline__ int needed_exp(float amax) {
   const uint32_t u = __float_as_uint(amax);
@@ -129,15 +138,14 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// N codes (4 or 8) of consecutive elements
+// N (4 or 8) codes of consecutive elements, given as pairs
 template <int N>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float* f) {
-  uint32_t w[N / 4];
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i)
-    w[i] = fp8::from_float2(f[4 * i], f[4 * i + 1]) | (fp8::from_float2(f[4 * i + 2], f[4 * i + 3]) << 16);
-  if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(p) = w[0];
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t* pairs) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(pairs[0] | (pairs[1] << 16), pairs[2] | (pairs[3] << 16));
+  else
+    *reinterpret_cast<uint32_t*>(p) = pairs[0] | (pairs[1] << 16);
 }
 
 // The page's live codes of one kv head (rows of D bytes, offsets `keep`) from
@@ -165,39 +173,39 @@ __device__ __forceinline__ void regrow(uint8_t* rows, uint32_t keep, int old, in
   }
 }
 
-// One head's rows of a page, ITS steps of them per lane: `value(it, x)` gives the N
-// elements this lane holds of step it's row (from registers; called twice, which
-// costs less than keeping the results would in resident warps).  Finds the exponent,
-// moves the live codes, and lets `put(it, x)` write the scaled elements.
-template <int D, int ITS, int N, typename Value, typename Put>
-__device__ __forceinline__ void quantise(const bool (&mine)[ITS], uint8_t* codes, uint8_t* scale,
-                                         uint32_t keep, int lane, Value value, Put put) {
+// The exact rotation of one vector of pairs, read again (rarely needed: out of the
+// way of the registers): its largest magnitude, and, where `codes` is given, its
+// codes for scale 2^ex.  Pair e is elements e and H + e at src, angle e at ang[e * UL].
+template <typename T, int H, int VEC, int UL>
+__device__ __noinline__ float exact_pairs(const T* src, const Angle* ang, uint8_t* codes, int ex) {
   float amax = 0.f;
-#pragma unroll
-  for (int it = 0; it < ITS; ++it)
-    if (mine[it]) {
-      float x[N];
-      value(it, x);
-#pragma unroll
-      for (int e = 0; e < N; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll 1
+  for (int e = 0; e < VEC; ++e) {
+    const Angle t = ang[e * UL];
+    const float a = Elem<T>::to_f(src[e]), b = Elem<T>::to_f(src[H + e]);
+    const float x = rot_odd(a, t.ch, t.cl, b, t.sh, t.sl);
+    const float y = rot_odd(b, t.ch, t.cl, -a, t.sh, t.sl);
+    amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+    if (codes) {
+      codes[e] = uint8_t(fp8::from_float2(fp8::scale2(x, -ex), 0.f));
+      codes[H + e] = uint8_t(fp8::from_float2(fp8::scale2(y, -ex), 0.f));
     }
+  }
+  return amax;
+}
+
+// What happens to one head's codes of a page once the largest new magnitude, or a
+// bound of it, is known: the exponent, the live codes moved, the scale written.
+template <int D>
+__device__ __forceinline__ int settle(int ex, uint8_t* codes, uint8_t* scale, uint32_t keep, int lane) {
   const int old = int(*scale) - fp8::kBias;
-  int ex = needed_exp(warp_max(amax));
   if (keep) {
     ex = max(ex, old);
     if (ex > old) regrow<D>(codes, keep, old, ex, lane);
   }
   __syncwarp();  // every lane has read the old scale
   if (lane == 0) *scale = uint8_t(ex + fp8::kBias);
-#pragma unroll
-  for (int it = 0; it < ITS; ++it)
-    if (mine[it]) {
-      float x[N];
-      value(it, x);
-#pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = fp8::scale2(x[e], -ex);
-      put(it, x);
-    }
+  return ex;
 }
 
 }  // namespace ak
@@ -227,6 +235,7 @@ __global__ void __launch_bounds__(ak::THREADS, sizeof(T) * MAXR <= 32 ? 3 : size
   // the angles come from the plan's own data (uploaded before any kernel of the
   // pass): while the kernel before this one may still run
   const int ang0 = is_k ? 0 : unit0 / Hq, ang1 = is_k ? wb.nrows : is_v ? 0 : (unit0 + units - 1) / Hq + 1;
+#pragma unroll 4
   for (int j = threadIdx.x; j < (ang1 - ang0) * H; j += THREADS) {
     const int i = j / H, f = j % H;
     const uint64_t turns = uint64_t(uint32_t(m.wpos[wb.row0 + ang0 + i])) * m.rope_turn[f];
@@ -253,21 +262,37 @@ __global__ void __launch_bounds__(ak::THREADS, sizeof(T) * MAXR <= 32 ? 3 : size
 
   if (!is_k && !is_v) {
     // ---- query heads, frozen rows included
-    for (int j = threadIdx.x; j < units * UL; j += THREADS) {
-      const int u = unit0 + j / UL, c = j % UL;
-      const int i = u / Hq;
-      const int64_t at = (int64_t(rows[i]) * Hq + u % Hq) * D + c * VEC;
+    // (all of a thread's vectors on their way before the first is turned)
+    constexpr int ITS = QUNITS * UL / THREADS;
+    static_assert(QUNITS * UL % THREADS == 0, "whole steps");
+    uint4 raw[ITS][2];
+    int64_t at[ITS];
+    int row[ITS];
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) {
+      const int j = threadIdx.x + it * THREADS, u = unit0 + j / UL;
+      row[it] = j < units * UL ? u / Hq : -1;
+      at[it] = 0;
+      if (row[it] >= 0) {
+        at[it] = (int64_t(rows[row[it]]) * Hq + (u - row[it] * Hq)) * D + j % UL * VEC;
+        raw[it][0] = *reinterpret_cast<const uint4*>(q + at[it]);
+        raw[it][1] = *reinterpret_cast<const uint4*>(q + at[it] + H);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) {
+      if (row[it] < 0) continue;
       float x[VEC], y[VEC], lo[VEC], hi[VEC];
-      unpack16<T>(*reinterpret_cast<const uint4*>(q + at), x);
-      unpack16<T>(*reinterpret_cast<const uint4*>(q + at + H), y);
+      unpack16<T>(raw[it][0], x);
+      unpack16<T>(raw[it][1], y);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const Angle& a = ang[(i - ang0) * H + e * UL + c];
+        const Angle& a = ang[(row[it] - ang0) * H + e * UL + threadIdx.x % UL];
         lo[e] = fmaf(x[e], a.ch, -(y[e] * a.sh));
         hi[e] = fmaf(y[e], a.ch, x[e] * a.sh);
       }
-      *reinterpret_cast<uint4*>(q_rot + at) = pack16<T>(lo);
-      *reinterpret_cast<uint4*>(q_rot + at + H) = pack16<T>(hi);
+      *reinterpret_cast<uint4*>(q_rot + at[it]) = pack16<T>(lo);
+      *reinterpret_cast<uint4*>(q_rot + at[it] + H) = pack16<T>(hi);
     }
     return;
   }
@@ -308,24 +333,71 @@ __global__ void __launch_bounds__(ak::THREADS, sizeof(T) * MAXR <= 32 ? 3 : size
         raw[it][1] = *reinterpret_cast<const uint4*>(src + H);
       }
     }
-    quantise<D, ITS, 2 * VEC>(
-        mine, codes, k_scale + cell, keep, lane,
-        [&](int it, float* x) {  // the rotated row's low part, then its high part
-          const int i = it * RPI + lane / UL;
-          float a[VEC], b[VEC];
-          unpack16<T>(raw[it][0], a);
-          unpack16<T>(raw[it][1], b);
+    // row of step `it`, rotated plainly or exactly, two elements e of it a time
+    auto angle_of = [&](int it, int e) -> const Angle& {
+      return ang[(it * RPI + lane / UL) * H + e * UL + c];
+    };
+    float amax = 0.f;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const Angle t = ang[i * H + e * UL + c];
-            x[e] = rot_odd(a[e], t.ch, t.cl, b[e], t.sh, t.sl);
-            x[VEC + e] = rot_odd(b[e], t.ch, t.cl, -a[e], t.sh, t.sl);
+    for (int it = 0; it < ITS; ++it)
+      if (mine[it]) {
+        float a[VEC], b[VEC];
+        unpack16<T>(raw[it][0], a);
+        unpack16<T>(raw[it][1], b);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 t = make_float2(angle_of(it, e).ch, angle_of(it, e).sh);
+          amax = fmaxf(amax, fmaxf(fabsf(fmaf(a[e], t.x, -(b[e] * t.y))),
+                                   fabsf(fmaf(b[e], t.x, a[e] * t.y))));
+        }
+      }
+    amax = warp_max(amax);
+    // (the largest magnitude is at least |x| + |y| over 2 for every pair)
+    int ex = needed_exp(amax * (1.f - 4.f * kRotErr));
+    if (ex != needed_exp(amax * (1.f + 4.f * kRotErr))) {
+      amax = 0.f;
+#pragma unroll 1
+      for (int i = lane / UL; i < wb.nrows; i += RPI)
+        if (slot0 + offs[i] >= frozen)
+          amax = fmaxf(amax, exact_pairs<T, H, VEC, UL>(k + (int64_t(rows[i]) * Hkv + g) * D + c * VEC,
+                                                        ang + i * H + c, nullptr, 0));
+      ex = needed_exp(warp_max(amax));
+    }
+    ex = settle<D>(ex, codes, k_scale + cell, keep, lane);
+#pragma unroll
+    for (int it = 0; it < ITS; ++it)
+      if (mine[it]) {
+        float a[VEC], b[VEC], lo[2][VEC], hi[2][VEC];
+        unpack16<T>(raw[it][0], a);
+        unpack16<T>(raw[it][1], b);
+        const float err = fp8::scale2(kRotErr, -ex);
+        bool sure = true;
+        uint32_t code[2][VEC / 2];  // pairs of codes of either half
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 t = make_float2(angle_of(it, e).ch, angle_of(it, e).sh);
+          const float x = fp8::scale2(fmaf(a[e], t.x, -(b[e] * t.y)), -ex);
+          const float y = fp8::scale2(fmaf(b[e], t.x, a[e] * t.y), -ex);
+          const float off = (fabsf(a[e]) + fabsf(b[e])) * err;
+          lo[0][e] = x - off, hi[0][e] = x + off;
+          lo[1][e] = y - off, hi[1][e] = y + off;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) {
+            code[h][e / 2] = fp8::from_float2(lo[h][e], lo[h][e + 1]);
+            sure = sure && code[h][e / 2] == fp8::from_float2(hi[h][e], hi[h][e + 1]);
           }
-        },
-        [&](int it, const float* x) {
-          store_codes<VEC>(codes + off[it] * D + c * VEC, x);
-          store_codes<VEC>(codes + off[it] * D + H + c * VEC, x + VEC);
-        });
+        uint8_t* row = codes + off[it] * D + c * VEC;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) store_codes<VEC>(row + h * H, code[h]);
+        if (!sure) {
+          const int i = it * RPI + lane / UL;
+          exact_pairs<T, H, VEC, UL>(k + (int64_t(rows[i]) * Hkv + g) * D + c * VEC, ang + i * H + c,
+                                     row, ex);
+        }
+      }
   } else {
     constexpr int VLN = D / VEC, RPI = 32 / VLN, ITS = MAXR / RPI;
     const int c = lane % VLN;
@@ -342,10 +414,27 @@ __global__ void __launch_bounds__(ak::THREADS, sizeof(T) * MAXR <= 32 ? 3 : size
       if (mine[it])
         raw[it] = *reinterpret_cast<const uint4*>(v + (int64_t(rows[i]) * Hkv + g) * D + c * VEC);
     }
-    quantise<D, ITS, VEC>(
-        mine, codes, v_scale + cell, keep, lane,
-        [&](int it, float* x) { unpack16<T>(raw[it], x); },
-        [&](int it, const float* x) { store_codes<VEC>(codes + off[it] * D + c * VEC, x); });
+    float amax = 0.f;
+#pragma unroll
+    for (int it = 0; it < ITS; ++it)
+      if (mine[it]) {
+        float x[VEC];
+        unpack16<T>(raw[it], x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(x[e]));
+      }
+    const int ex = settle<D>(needed_exp(warp_max(amax)), codes, v_scale + cell, keep, lane);
+#pragma unroll
+    for (int it = 0; it < ITS; ++it)
+      if (mine[it]) {
+        float x[VEC];
+        uint32_t code[VEC / 2];
+        unpack16<T>(raw[it], x);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2)
+          code[e / 2] = fp8::from_float2(fp8::scale2(x[e], -ex), fp8::scale2(x[e + 1], -ex));
+        store_codes<VEC>(codes + off[it] * D + c * VEC, code);
+      }
   }
 }
 
