@@ -166,10 +166,12 @@ def copy_pages(pools, src, dst, status=None, stream=None) -> None:
     status_p = p(status, "status", None, 4)
     # (a model has dozens of pools: each check one pass over all of them)
     pools, T = list(pools), torch.Tensor
-    if not all(map(T.dim, pools)) or not all(map(T.is_contiguous, pools)) or \
-            any(d != p.device for d in map(T.get_device, pools)):
-        raise ValueError("a pool must be a contiguous tensor of pages on the current CUDA device")
-    counts = set(map(T.size, pools, itertools.repeat(0)))
+    try:
+        counts = set(map(T.size, pools, itertools.repeat(0)))
+    except IndexError:
+        raise ValueError("a pool must have a dimension of pages") from None
+    if not all(map(T.is_contiguous, pools)) or any(d != p.device for d in map(T.get_device, pools)):
+        raise ValueError("a pool must be contiguous and on the current CUDA device")
     if len(counts) > 1:
         raise ValueError("the pools must have the same number of pages")
     pages = counts.pop() if counts else 0
