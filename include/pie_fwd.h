@@ -425,7 +425,8 @@ typedef struct pie_fwd_cache {
  * and those from the first row's window on; pages in between are never read,
  * so their page-table entries may name any page of the pool.
  * Errors beside pie_fwd_plan's: PIE_EINVAL for an unknown kv_type, sinks
- * without a window, a window together with a mask, or (PIE_KV_E4M3) two
+ * without a window, a window together with a mask, an sm_scale below zero or
+ * not finite, or (PIE_KV_E4M3) two
  * page-table entries of the pass that write one physical page (its slots share
  * a scale); PIE_ERANGE for a negative window or sinks. */
 int pie_fwd_cache_workspace_bytes(const pie_fwd_desc* desc, const pie_fwd_cache* cache,

@@ -139,7 +139,8 @@ def forward_cache(desc: abi.pie_fwd_desc, cache: abi.pie_fwd_cache, meta: _HostM
     c = meta.c
     # (readouts by default: the last row of every lane that has rows)
     n_ro = c.num_readout if c.readout else int(np.count_nonzero(np.diff(meta.keep["row_indptr"])))
-    z, p = _Shapes(desc, c, n_ro), _Args(stream)
+    z, p = _Shapes(desc, meta, n_ro), _Args(stream)
+    z.check_mask(mask_words)
     pool = 1 if kv8 else z.dt
     abi.check(abi.load().pie_fwd_forward_cache(
         C.byref(desc), C.byref(cache), C.byref(c), p(workspace, "workspace", None, 1),
@@ -175,6 +176,8 @@ def copy_pages(pools, src, dst, status=None, stream=None) -> None:
     if len(counts) > 1:
         raise ValueError("the pools must have the same number of pages")
     pages = counts.pop() if counts else 0
+    if max(pages, n_pairs) >= 1 << 31:
+        raise ValueError("page numbers and pairs are 32-bit numbers")
     ptrs, sizes = list(map(T.data_ptr, pools)), [t.nbytes for t in pools]
     if 0 in sizes:  # (a pool whose pages hold nothing has nothing to copy)
         ptrs, sizes = [a for a, b in zip(ptrs, sizes) if b], [b for b in sizes if b]
@@ -290,9 +293,11 @@ class _Args:
 class _Shapes:
     """The shapes and types of a pass's tensors, made once per plan."""
 
-    def __init__(self, desc, c, num_readout: int):
+    def __init__(self, desc, meta, num_readout: int):
         import torch
-        size = torch.Size
+        size, c = torch.Size, meta.c
+        indptr = meta.keep["mask_word_indptr"]
+        self.mask_words = 0 if indptr is None or not len(indptr) else int(indptr[-1])
         N, Hq, Hkv, d = c.num_rows, desc.num_q_heads, desc.num_kv_heads, desc.head_dim
         self.dt = torch.bfloat16 if desc.dtype == PIE_BF16 else torch.float32
         self.f32, self.i32 = torch.float32, torch.int32
@@ -302,6 +307,10 @@ class _Shapes:
         self.pool = size((c.num_pool_pages, Hkv, desc.page_size, d))
         self.scale = size((c.num_pool_pages, Hkv))
         self.lanes = size((c.num_lanes,))
+
+    def check_mask(self, mask_words) -> None:
+        if mask_words is not None and mask_words.numel() < self.mask_words:
+            raise ValueError(f"mask_words must hold {self.mask_words} words, not {mask_words.numel()}")
 
 
 def _stream(stream):
@@ -339,7 +348,7 @@ class ForwardPlan:
             "pie_fwd_plan")
         self.handle = h
         self.num_readout = int(self.lib.pie_fwd_plan_num_readout(h))
-        self._shapes = _Shapes(desc, meta.c, self.num_readout) if cache is not None else None
+        self._shapes = _Shapes(desc, meta, self.num_readout) if cache is not None else None
 
     @classmethod
     def _adopt(cls, handle, desc: abi.pie_fwd_desc, workspace):
@@ -355,10 +364,13 @@ class ForwardPlan:
         self._shapes = None  # (a plan of the pass dtype)
         return self
 
-    def _kv8_shapes(self) -> "_Shapes":
+    def _kv8_args(self, stream):
         if self._shapes is None:
             raise ValueError("the plan was made without a cache (see make_cache)")
-        return self._shapes
+        p = _Args(stream)
+        if self.workspace.get_device() != p.device:
+            raise ValueError("the plan's workspace is not on the current CUDA device")
+        return self._shapes, p
 
     def append_kv(self, q, k, v, q_rot, k_pool, v_pool, frozen_len, status=None, stream=None):
         abi.check(self.lib.pie_fwd_append_kv(
@@ -385,7 +397,7 @@ class ForwardPlan:
                    stream=None):
         """pie_fwd_append_kv8: k_pool / v_pool [pages, Hkv, P, d] e4m3 codes (any
         1-byte dtype), k_scale / v_scale [pages, Hkv] E8M0 bytes."""
-        z, p = self._kv8_shapes(), _Args(stream)
+        z, p = self._kv8_args(stream)
         abi.check(self.lib.pie_fwd_append_kv8(
             self.handle, p(q, "q", z.q, z.dt), p(k, "k", z.kv, z.dt), p(v, "v", z.kv, z.dt),
             p(q_rot, "q_rot", z.q, z.dt), p(k_pool, "k_pool", z.pool, 1),
@@ -397,7 +409,8 @@ class ForwardPlan:
                    out_readout=None, lse_readout=None, out_all=None, lse_all=None, status=None,
                    stream=None):
         """pie_fwd_attend_kv8: attend() over the codes and scales of append_kv8."""
-        z, p = self._kv8_shapes(), _Args(stream)
+        z, p = self._kv8_args(stream)
+        z.check_mask(mask_words)
         abi.check(self.lib.pie_fwd_attend_kv8(
             self.handle, p(q_rot, "q_rot", z.q, z.dt), p(k_pool, "k_pool", z.pool, 1),
             p(v_pool, "v_pool", z.pool, 1), p(k_scale, "k_scale", z.scale, 1),

@@ -220,7 +220,8 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
       return fail(PIE_EINVAL, "a pass has a window or a mask, not both");
     H.kv8 = cache->kv_type == PIE_KV_E4M3;
     H.window = cache->window;
-    H.sinks = cache->sinks;
+    // (past every slot, and its pages' slots still a 32-bit number)
+    H.sinks = std::min(cache->sinks, INT32_MAX - 63);
   }
   const pie_fwd_desc& D = *desc;
   const pie_fwd_meta& M = *meta;

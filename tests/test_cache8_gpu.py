@@ -504,3 +504,25 @@ def test_copy_pages_refusals():
             pk.copy_pages(pools, src, dst)
     pk.copy_pages([], i, i)
     pk.copy_pages([pool], i[:0], i[:0])
+
+
+def test_too_few_mask_words_and_too_many_pages_are_refused():
+    import programmable_paged_kv_gb300 as pk
+    desc = W.Desc(4, 2, 64, 16, W.BF16)
+    p, pages, (q, k, v), pool = _state(96, desc, [CC.tail(100, 2)],
+                                       mask=lambda rng, l, r, kv: np.ones(kv, bool))
+    plan = CC.plan_of(desc, p, pages, kv="e4m3")
+    words, out = CC.mask_dev(p), torch.empty_like(q)
+    with pytest.raises(ValueError, match="mask_words"):
+        plan.attend_kv8(q, *pool, words[:-1], out_all=out)
+    plan.attend_kv8(q, *pool, words, out_all=out)
+    plan.close()
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="32-bit"):
+        pk.copy_pages([torch.empty((2 ** 31, 1), dtype=torch.uint8, device="cuda")], i, i)
+
+
+@pytest.mark.parametrize("desc", DESCS[:3], ids=str)
+def test_attend_sinks_past_every_slot(desc):
+    p, pages = CC.make_pass(97, desc, [CC.tail(400, 1), CC.tail(70, 6), CC.tail(333, 30)])
+    _check_attend(desc, p, pages, 98, 5, 2 ** 31 - 1)

@@ -104,3 +104,25 @@ def test_fork_copies_a_shared_page_before_either_branch_writes():
     O8.append(desc, p, CC.values(p.v, 1), host[1], host[3], [20, 20])
     for t, h in zip(dev, host):
         assert np.array_equal(t.cpu().numpy(), h)
+
+
+def test_captured_copies_replay_on_other_pairs():
+    import programmable_paged_kv_gb300 as pk
+    pools = _pools(64, 2)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    src, dst = i32([0, 1, 2]), i32([10, 11, 12])
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        pk.copy_pages(pools, src, dst, stream=stream)
+    for s, d in (([3, 3, 4], [20, 21, 22]), ([5, 6, 7], [5, 30, 31])):  # a source twice, a page to itself
+        src.copy_(i32(s))
+        dst.copy_(i32(d))
+        want = [p.clone() for p in pools]
+        for w in want:
+            w[d] = w[s]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(pools, want))

@@ -147,3 +147,45 @@ def test_windowed_pass_in_one_call():
         res.append((q_rot, kp, vp, out, lse, frozen))
     assert all(torch.equal(a, b) for a, b in zip(*res))
     assert res[0][-1].cpu().tolist() == [700, 90]
+
+
+@pytest.mark.parametrize("desc", DESCS, ids=str)
+def test_sinks_past_every_slot(desc):
+    p, pages = CC.make_pass(58, desc, [CC.tail(400, 1), CC.tail(70, 6), CC.tail(333, 30)])
+    _check(desc, p, pages, 59, 5, 2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("desc", DESCS[::2], ids=str)
+def test_captured_windowed_attention_replays(desc):
+    """One plan's windowed attention captured and replayed on other queries and
+    caches: the same bits as eager calls on them."""
+    p, pages = CC.make_pass(60, desc, [CC.tail(900, 1), CC.tail(70, 6), CC.tail(333, 100)])
+    plan = CC.plan_of(desc, p, pages, window=50, sinks=20)
+    dt = torch.float32 if desc.dtype == W.F32 else torch.bfloat16
+    q = torch.empty((len(p.slots), desc.num_q_heads, desc.head_dim), dtype=dt, device="cuda")
+    k, v = (torch.zeros((pages, desc.num_kv_heads, desc.page_size, desc.head_dim), dtype=dt,
+                        device="cuda") for _ in "kv")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    stream = torch.cuda.Stream()
+    run = lambda: plan.attend(q, k, v, None, None, None, out, lse, stream=stream)
+    torch.cuda.synchronize()
+    q.zero_()
+    torch.cuda.synchronize()
+    run()  # (first calls set the kernels' attributes)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        run()
+    for seed in range(2):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(seed)
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+        res = []
+        for replay in (True, False):
+            torch.cuda.synchronize()
+            graph.replay() if replay else run()
+            torch.cuda.synchronize()
+            res.append((out.clone(), lse.clone()))
+        assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+    plan.close()
