@@ -143,7 +143,9 @@ static int choose_chunk(int64_t total_slots_x_heads) {
 constexpr int kTcMinQueries = 16;
 
 // 8-bit caches: lanes with more query vectors per kv head than this use the
-// tensor-core kernel (bf16, d 128); up to it, items of kWideQueries.
+// tensor-core kernel (bf16, d 128); up to it, items of kWideQueries or fewer.  (48
+// lanes of 1,024 to 8,192 slots, 8 kv heads, wide items against the tensor-core
+// kernel: 16 vectors 157 and 165 us, 32 159 and 194, 64 265 and 201, 128 467 and 210.)
 constexpr int kTc8MinQueries = 32;
 
 // Multiprocessors of the current device, looked up once per device; the
@@ -415,10 +417,14 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
     return tc_ok && n > 0 && (n * G >= kTcMinQueries || (H.has_mask && !mma_ok));
   };
   auto lane_list = [&](int l) { return !H.kv8 && H.has_mask && (lane_tc(l) || mma_ok); };
-  // 8-bit caches: lanes with more query vectors per kv head than one item's 8
-  // take wide items, which convert each code once for up to 32 of them
+  // 8-bit caches: lanes that would take more than three items of up to 8 query
+  // vectors take wide items, which convert each code once for up to 32 of them.
+  // (48 lanes of 1,024 to 8,192 slots, 8 kv heads of 128, items of 8 against wide
+  // ones: 12 vectors 96 and 119 us, 16 115 and 155, 20 138 and 147, 24 164 and 153,
+  // 32 250 and 161.  fp32, 40 lanes, 4 kv heads of 64, items of 6: 15 vectors 57 and
+  // 68 us, 21 72 and 70, 24 101 and 75.)
   auto lane_wide = [&](int l) {
-    return H.kv8 && !lane_tc(l) && (M.row_indptr[l + 1] - M.row_indptr[l]) * G > 8;
+    return H.kv8 && !lane_tc(l) && M.row_indptr[l + 1] - M.row_indptr[l] > 3 * rows_per_item;
   };
   const int wide_rows = std::max(1, kWideQueries / G);
   // split-KV items: chunk length from the total work

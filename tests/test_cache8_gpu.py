@@ -320,12 +320,12 @@ def test_captured_pass_replays_on_changed_inputs():
     tensor-core items in one plan) and replayed on other inputs: the same bits as
     eager calls on them."""
     desc = W.Desc(8, 2, 128, 16, W.BF16)
-    p, pages, (q, k, v), pool = _state(60, desc, [CC.tail(300, 1), CC.tail(90, 5), CC.tail(200, 20)],
+    p, pages, (q, k, v), pool = _state(60, desc, [CC.tail(300, 1), CC.tail(90, 7), CC.tail(200, 20)],
                                        fold=[W.FOLD_ALL] * 3)
     plan = CC.plan_of(desc, p, pages, kv="e4m3")
     q_rot, out = torch.empty_like(q), torch.empty_like(q)
     lse = torch.empty(out.shape[:2], device="cuda")
-    frozen = CC.to_dev(np.array([299, 85, 180], np.int32))
+    frozen = CC.to_dev(np.array([299, 83, 180], np.int32))
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     stream = torch.cuda.Stream()
 
