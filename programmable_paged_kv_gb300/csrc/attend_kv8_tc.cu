@@ -347,12 +347,16 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
       }
       const int valid = min(BN, ke - tile_at(j));
       const uint8_t* src = S.raw[rs] + kv * BN * D;
-      uint4 u[BN / 8];
+      // (u[.][0] is the 8 codes stored first)
+      uint2 u[BN / 8][2];
 #pragma unroll
       for (int i = 0; i < BN / 8; ++i) {
         const int r = r0 + 8 * i;
-        u[i] = r < valid ? *reinterpret_cast<const uint4*>(src + r * D + c * 16)
-                         : make_uint4(0u, 0u, 0u, 0u);
+        u[i][0] = u[i][1] = make_uint2(0u, 0u);
+        if (r < valid) {
+          u[i][0] = *reinterpret_cast<const uint2*>(src + r * D + c * 16 + 8 * h);
+          u[i][1] = *reinterpret_cast<const uint2*>(src + r * D + c * 16 + 8 - 8 * h);
+        }
       }
       int ek = 0, ev = 0;
       if (kv == 0 && ct < BN / 8) {
@@ -373,13 +377,12 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
 #pragma unroll
       for (int i = 0; i < BN / 8; ++i) {
         uint32_t f[8];
-        fp8::to_half2x2(u[i].x, f[0], f[1]);
-        fp8::to_half2x2(u[i].y, f[2], f[3]);
-        fp8::to_half2x2(u[i].z, f[4], f[5]);
-        fp8::to_half2x2(u[i].w, f[6], f[7]);
-        const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), b = make_uint4(f[4], f[5], f[6], f[7]);
-        *reinterpret_cast<uint4*>(dst + i * 1024 + o0) = h ? b : a;
-        *reinterpret_cast<uint4*>(dst + i * 1024 + o1) = h ? a : b;
+        fp8::to_half2x2(u[i][0].x, f[0], f[1]);
+        fp8::to_half2x2(u[i][0].y, f[2], f[3]);
+        fp8::to_half2x2(u[i][1].x, f[4], f[5]);
+        fp8::to_half2x2(u[i][1].y, f[6], f[7]);
+        *reinterpret_cast<uint4*>(dst + i * 1024 + o0) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(dst + i * 1024 + o1) = make_uint4(f[4], f[5], f[6], f[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -559,34 +562,52 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
         tc::fence_after();
         const bool empty = !(l_run > 0.f);
         const float inv = empty ? 0.f : 1.f / l_run;
-        const int rd0 = m.ro_indptr[row], rd1 = m.ro_indptr[row + 1];
+        // Rows leave through the warp's part of the query tile (every product that
+        // read it has finished): a thread's own row is 16-byte chunks 256 bytes and
+        // more apart, 16 lanes' chunks of one row are whole lines.
+        uint8_t* rows_s = S.q[t][0] + quad * 32 * 256;
+        const int c = lane & 15, lg = fp8::log2i(G), q0 = t * kTcTileQueries + quad * 32;
+        auto chunk_of = [&](int r, int ch) -> uint4* {
+          return reinterpret_cast<uint4*>(rows_s + r * 256 + ((ch ^ (r & 15)) << 4));
+        };
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           float o[64];
           ld64(tO + 64 * hh, o);
-          if (valid_q && it.direct) {
-            uint4 w[8];
+          if (it.direct) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int ch = 0; ch < 8; ++ch) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[8 * c + e] *= inv;
-              w[c] = pack16<__nv_bfloat16>(o + 8 * c);
+              for (int e = 0; e < 8; ++e) o[8 * ch + e] *= inv;
+              *chunk_of(lane, 8 * hh + ch) = pack16<__nv_bfloat16>(o + 8 * ch);
             }
-            auto put = [&](__nv_bfloat16* base, int64_t r) {
-              uint4* dst = reinterpret_cast<uint4*>(base + (r * Hq + head) * D + 64 * hh);
+          } else {
 #pragma unroll
-              for (int c = 0; c < 8; ++c) dst[c] = w[c];
-            };
-            if (out.out_all) put(out.out_all, row);
-            if (out.out_readout)
-              for (int i = rd0; i < rd1; ++i) put(out.out_readout, m.ro_idx[i]);
-          } else if (valid_q) {
-            float4* po = reinterpret_cast<float4*>(m.part_o + int64_t(it.part_base + q) * D + 64 * hh);
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              po[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int ch = 0; ch < 16; ++ch)
+              *chunk_of(lane, ch) = make_uint4(__float_as_uint(o[4 * ch]), __float_as_uint(o[4 * ch + 1]),
+                                               __float_as_uint(o[4 * ch + 2]), __float_as_uint(o[4 * ch + 3]));
           }
+          if (it.direct && hh == 0) continue;
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4), qr = q0 + r;
+            if (qr >= nqv) break;
+            const uint4 w = *chunk_of(r, c);
+            if (it.direct) {
+              const int rw = it.row0 + (qr >> lg), hd = it.kv_head * G + (qr & (G - 1));
+              if (out.out_all)
+                *reinterpret_cast<uint4*>(out.out_all + (int64_t(rw) * Hq + hd) * D + 8 * c) = w;
+              if (out.out_readout)
+                for (int k = m.ro_indptr[rw]; k < m.ro_indptr[rw + 1]; ++k)
+                  *reinterpret_cast<uint4*>(out.out_readout + (int64_t(m.ro_idx[k]) * Hq + hd) * D + 8 * c) = w;
+            } else {
+              *reinterpret_cast<uint4*>(m.part_o + int64_t(it.part_base + qr) * D + 64 * hh + 4 * c) = w;
+            }
+          }
+          __syncwarp();
         }
+        const int rd0 = m.ro_indptr[row], rd1 = m.ro_indptr[row + 1];
         if (valid_q) {
           if (it.direct) {
             const float lse = empty ? -INFINITY : (m_used + log2f(l_run)) * kLn2;
