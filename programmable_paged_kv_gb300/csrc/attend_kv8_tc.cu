@@ -23,11 +23,21 @@
 //                 lane); first they write the scaled query vectors into the operand
 //                 tile.  With two query tiles they take registers over
 //                 from the other warps (128 each at launch; 168 and 88).
-// Scores of tile j + 2 are issued behind P.V of tile j, so a softmax step never
-// waits for them.  The conversion costs 1 shared load, 8 conversions and 2
-// shared stores per 16 codes, about a third of the softmax's issue slots with
-// NT = 2, and runs beside it.  Masked passes walk only the tiles some row of the
-// item sees, listed once at the start.  Every wait is bounded in time.
+// Scores of tile j + 2 are issued behind P.V of tile j.  Masked passes walk only
+// the tiles some row of the item sees, listed once at the start.  Every wait is
+// bounded in time.
+//
+// What bounds it: shared memory.  With NT = 2 a tile moves 96 KB of score operands
+// (8 steps of d, 4 KB of Q and 2 KB of K each, twice), 32 KB of V, and 64 KB
+// through the converters (16 in, 16 out, 32 written): 1,540 of the 2,250 cycles
+// between two tiles at 128 bytes per cycle.  The tensor cores' products
+// need 1,020 of them, the softmax warps 1,600 each (64 exponentials a row).  The set-up
+// (the page look-ups, the first copies, the queries' powers of two) and the
+// way out take 13,000 cycles per item.
+// 64 lanes x 64 rows over 1,088 slots (32 + 8 heads, bf16): 114 us, 620 TFLOP/s of
+// the 1,868 that a dense product reaches.  (Products of the codes as they are, at
+// e4m3's double rate, would need queries and weights in two parts each, which
+// takes the doubling back.)
 
 #include <cfloat>
 #include <climits>
@@ -164,6 +174,10 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
   extern __shared__ uint8_t smem_raw[];
   Smem<NT>& S = *reinterpret_cast<Smem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
+  if (threadIdx.x == 32) {  // (the maps are kernel parameters, not in any cache yet)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+  }
   const TcItem it = m.tc_items[blockIdx.x];
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int kb = it.kv_begin, ke = it.kv_end;

@@ -444,7 +444,9 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
   int CH = choose_chunk(work);
   // 8-bit caches and windows: where that gives less than about four waves of the
   // three CTAs per SM, the chunk that makes the waves' time shortest, an item costing
-  // its slots and about kItemSlots more (its first copies, its partials).
+  // its slots and about kItemSlots more (its first copies, its partials).  (Without
+  // and with: 8 windowed lanes of 4,100 slots 36 and 31 us, 33 of 1,033 8-bit
+  // slots 15.5 and 12.4, the 64-lane decode batch 58 either way.)
   if (H.kv8 || H.window > 0) {
     const int kItemSlots = 192;
     static thread_local std::vector<int32_t> exts;
@@ -504,31 +506,43 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
                   : std::max<int64_t>(512, (tc_total + tc_target - 1) / tc_target);
   // 8-bit caches and windows: the chunk that makes the time of the busiest SM
   // shortest, an item costing its 64-slot tiles and about kItemTiles more (set-up,
-  // queries, the first copies, the outputs).  Few items run in whole waves;
-  // many balance, up to half of the longest one.
+  // queries, the first copies, the outputs), and, where a row block is split, its
+  // partials' way to memory and back, about kPartTiles for 256 query vectors.  Few
+  // items run in whole waves; many balance, up to half of the longest one.  (Four
+  // waves of items, as above, against this: 8 windowed lanes of 64 rows 77 and 57
+  // us, 48 of 500 to 6,000 slots 213 and 157, 48 lanes of 64 rows over 1,024 to
+  // 8,192 8-bit slots 311 and 236; kPartTiles 0 gave 200 and 309 there, 3 and 10
+  // what 6 gives.)
   if ((H.kv8 || H.window > 0) && tc_units > 0) {
-    const int kItemTiles = 5;
-    static thread_local std::vector<int32_t> exts;
-    exts.clear();
+    const int kItemTiles = 5, kPartTiles = 6;
+    struct Unit {
+      int32_t ext, queries;
+    };
+    static thread_local std::vector<Unit> units;
+    units.clear();
     int longest = 1;
     for (int l = 0; l < L; ++l) {
       if (!lane_tc(l)) continue;
       const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1];
       for (int b0 = r0; b0 < r1; b0 += tc_rows) {
         int skip;
-        exts.push_back(reads(l, b0, std::min(r1, b0 + tc_rows), &skip));
-        longest = std::max(longest, exts.back());
+        const int b1 = std::min(r1, b0 + tc_rows);
+        units.push_back({reads(l, b0, b1, &skip), (b1 - b0) * G});
+        longest = std::max(longest, units.back().ext);
       }
     }
     double best = 0.0;
     int best_n = 0;
     for (int n = 1; n <= 64 && (n == 1 || longest / n >= 256); ++n) {
       const int64_t ch = (longest + n - 1) / n;
-      int64_t items = 0, tiles = 0;
-      for (const int32_t e : exts) {
-        items += std::max<int64_t>(1, (e + ch / 2) / ch);
-        tiles += (e + 63) / 64;
+      int64_t items = 0, tiles = 0, parts = 0;
+      for (const Unit& u : units) {
+        const int64_t chunks = std::max<int64_t>(1, (u.ext + ch / 2) / ch);
+        items += chunks;
+        tiles += (u.ext + 63) / 64;
+        if (chunks > 1) parts += chunks * u.queries;
       }
+      tiles += parts * kPartTiles / 256;
       items *= Hkv;
       tiles *= Hkv;
       const double mean = static_cast<double>(tiles) / items + kItemTiles;
@@ -644,7 +658,9 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
     std::stable_sort(H.dec.begin(), H.dec.end(), [](const DecItem& a, const DecItem& b) {
       return (a.block >= 0 ? a.kv_begin : 0) < (b.block >= 0 ? b.kv_begin : 0);
     });
-  // the longest tensor-core items first, so that the short ones fill the end
+  // the longest tensor-core items first, so that the short ones fill the end (64
+  // lanes of 64 rows over 100 to 2,000 8-bit slots: 115 us in the lanes' order, 103
+  // so; 16 rows, whose chunks are much alike, 218 and 223)
   if ((H.kv8 || H.window > 0) && !H.tc.empty())
     std::stable_sort(H.tc.begin(), H.tc.end(), [](const TcItem& a, const TcItem& b) {
       return a.kv_end - a.kv_begin > b.kv_end - b.kv_begin;
