@@ -345,12 +345,12 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
     // ---------------- converters -------------------------------------------------
     // Warps 4, 5 take K, 6 and 7 V.  Thread: 16-byte chunk c of rows r0, r0 + 8,
     // ..; its 16 codes become two 16-byte chunks of the operand row (half c / 4
-    // of d).  The upper half's threads write their two chunks in the other order,
-    // so that the 8 threads of a row's store hit 8 distinct banks.  The raw stage
+    // of d).  Which of the two is first alternates with the half (the 8 threads of a
+    // row's store hit 8 distinct banks) and with the row (so do two rows' loads). The raw stage
     // is released as soon as its codes are in registers.
     const int kv = (warp - C::kConv0) >> 1;
     const int ct = (threadIdx.x - 32 * C::kConv0) & 63;
-    const int c = ct & 7, r0 = ct >> 3, h = c >> 2;
+    const int c = ct & 7, r0 = ct >> 3, h = c >> 2, first = h ^ (r0 & 1);
     const int lp = fp8::log2i(P);
     uint64_t* done = kv ? S.v_full : S.k_full;
     for (int j = 0; j < T; ++j) {
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
         const int r = r0 + 8 * i;
         u[i][0] = u[i][1] = make_uint2(0u, 0u);
         if (r < valid) {
-          u[i][0] = *reinterpret_cast<const uint2*>(src + r * D + c * 16 + 8 * h);
-          u[i][1] = *reinterpret_cast<const uint2*>(src + r * D + c * 16 + 8 - 8 * h);
+          u[i][0] = *reinterpret_cast<const uint2*>(src + r * D + c * 16 + 8 * first);
+          u[i][1] = *reinterpret_cast<const uint2*>(src + r * D + c * 16 + 8 - 8 * first);
         }
       }
       int ek = 0, ev = 0;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(t8::Cfg<NT>::kThreads, 1) attend_kv8_tc_kernel
         S.sc[st][ct] = make_float4(fp8::pow2i(ek), float(ev), fp8::pow2i(-ev), 0.f);
       uint8_t* dst = (kv ? S.v[st][h] : S.k[st][h]) + r0 * 128;
       const int dc = 2 * (c & 3);
-      const int o0 = ((dc + h) ^ (r0 & 7)) << 4, o1 = ((dc + 1 - h) ^ (r0 & 7)) << 4;
+      const int o0 = ((dc + first) ^ (r0 & 7)) << 4, o1 = ((dc + 1 - first) ^ (r0 & 7)) << 4;
 #pragma unroll
       for (int i = 0; i < BN / 8; ++i) {
         uint32_t f[8];
