@@ -9,6 +9,7 @@ if the library is missing every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import itertools
 import types
@@ -171,21 +172,22 @@ def copy_pages(pools, src, dst, status=None, stream=None) -> None:
         counts = set(map(T.size, pools, itertools.repeat(0)))
     except IndexError:
         raise ValueError("a pool must have a dimension of pages") from None
-    if not all(map(T.is_contiguous, pools)) or any(d != p.device for d in map(T.get_device, pools)):
+    if (not all(map(T.is_contiguous, pools))
+            or list(map(T.get_device, pools)).count(p.device) != len(pools)):
         raise ValueError("a pool must be contiguous and on the current CUDA device")
     if len(counts) > 1:
         raise ValueError("the pools must have the same number of pages")
     pages = counts.pop() if counts else 0
     if max(pages, n_pairs) >= 1 << 31:
         raise ValueError("page numbers and pairs are 32-bit numbers")
-    ptrs, sizes = list(map(T.data_ptr, pools)), [t.nbytes for t in pools]
-    if 0 in sizes:  # (a pool whose pages hold nothing has nothing to copy)
-        ptrs, sizes = [a for a, b in zip(ptrs, sizes) if b], [b for b in sizes if b]
-    if not ptrs or n_pairs == 0:
+    if pages == 0 or n_pairs == 0:
         return
-    ptrs, sizes = np.array(ptrs, np.uint64), np.array(sizes, np.int64) // pages
-    abi.check(abi.load().pie_fwd_copy_pages(ptrs.size, ptrs.ctypes.data, sizes.ctypes.data, pages,
-                                            n_pairs, src_p, dst_p, status_p, p.stream),
+    # (a pool whose pages hold nothing has nothing to copy)
+    pools = [t for t in pools if t.nbytes] if 0 in map(T.numel, pools) else pools
+    ptrs = array.array("Q", map(T.data_ptr, pools))
+    sizes = array.array("q", [t.nbytes // pages for t in pools])
+    abi.check(abi.load().pie_fwd_copy_pages(len(pools), ptrs.buffer_info()[0], sizes.buffer_info()[0],
+                                            pages, n_pairs, src_p, dst_p, status_p, p.stream),
               "pie_fwd_copy_pages")
 
 
