@@ -67,7 +67,7 @@ namespace a8 {
 constexpr int WARPS = 4;
 constexpr int THREADS = (WARPS + 1) * 32;
 constexpr int MAX_PAGES = kStageSlots / 8;  // pages per stage at most
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 // Geometry of a kernel for items of NQ query vectors whose warps come to a stage in
 // groups of READERS.
@@ -393,6 +393,38 @@ __device__ __forceinline__ void load_q(const Shared<C>& S, int nt, int kk, uint3
   }
 }
 
+template <typename T>
+struct Outs {
+  T* out_readout;
+  float* lse_readout;
+  T* out_all;
+  float* lse_all;
+};
+
+// Elements 2c and 2c + 1 of query vector q of an item that covers its rows' whole
+// visible range: sums O over the weights' sum (and the lse, with the first two).
+template <typename T, int D>
+__device__ __forceinline__ void put_out(const DevMeta& m, const Outs<T>& out, const DecItem& it, int Hq,
+                                        int G, int q, int c, float2 O, float M, float sum) {
+  const int row = it.row0 + q / G, head = it.kv_head * G + q % G;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float lse = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  auto put = [&](T* o, float* l, int64_t at) {
+    if (o) {
+      T* dst = o + at * D + 2 * c;
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float2*>(dst) = make_float2(O.x * inv, O.y * inv);
+      else
+        *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(O.x * inv, O.y * inv);
+    }
+    if (l && c == 0) l[at] = lse;
+  };
+  put(out.out_all, out.lse_all, int64_t(row) * Hq + head);
+  if (out.out_readout || out.lse_readout)
+    for (int i = m.ro_indptr[row]; i < m.ro_indptr[row + 1]; ++i)
+      put(out.out_readout, out.lse_readout, int64_t(m.ro_idx[i]) * Hq + head);
+}
+
 // The slots that every query vector of an item sees.
 struct Common {
   int lim_min, lim_max;
@@ -441,7 +473,7 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
                       const uint8_t* k_scale, const uint8_t* v_scale, const uint32_t* mask_words,
                       const DecItem* items, int num_items, int* work, uint32_t* status,
                       const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap) {
+                      const __grid_constant__ CUtensorMap vmap, a8::Outs<T> out) {
   using namespace a8;
   constexpr bool SPLIT = sizeof(T) == 4;
   using C = NarrowCfg<D, SPLIT>;
@@ -649,10 +681,15 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
     // (pairs of elements XORed by the query, so that 4 rows' stores hit distinct
     // banks)
     if (gs == gs0) {  // no slot: empty states
-      for (int i = threadIdx.x; i < nqv * D; i += WARPS * 32) {
-        const int64_t at = int64_t(it.part_base) + i / D;
-        m.part_o[at * D + i % D] = 0.f;
-        if (i % D == 0) m.part_ml[at] = make_float2(-INFINITY, 0.f);
+      for (int i = threadIdx.x; i < nqv * (D / 2); i += WARPS * 32) {
+        const int qq = i / (D / 2), c = i % (D / 2);
+        if (it.part_base < 0) {
+          put_out<T, D>(m, out, it, Hq, G, qq, c, make_float2(0.f, 0.f), 0.f, 0.f);
+          continue;
+        }
+        const int64_t at = int64_t(it.part_base) + qq;
+        reinterpret_cast<float2*>(m.part_o + at * D)[c] = make_float2(0.f, 0.f);
+        if (c == 0) m.part_ml[at] = make_float2(-INFINITY, 0.f);
       }
       continue;
     }
@@ -675,28 +712,39 @@ __global__ void __launch_bounds__(a8::THREADS, 3)
       for (int n = 0; n < KS; ++n) orow[(8 * n + g) ^ (t << 2)] = make_float2(o[n][i], o[n][2 + i]);
     }
     sync_compute();
-    for (int i = threadIdx.x; i < nqv * (D / 2); i += WARPS * 32) {
-      const int qq = i / (D / 2), c = i % (D / 2);
-      float M = -INFINITY;
+    // (two loops: with the choice inside, the decode batch took 0.4 us longer)
+    auto merge = [&](auto put) {
+      for (int i = threadIdx.x; i < nqv * (D / 2); i += WARPS * 32) {
+        const int qq = i / (D / 2), c = i % (D / 2);
+        float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mw[w * 8 + qq]);
-      float2 O = make_float2(0.f, 0.f);
-      float Ls = 0.f;
-      if (M != -INFINITY) {
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mw[w * 8 + qq]);
+        float2 O = make_float2(0.f, 0.f);
+        float Ls = 0.f;
+        if (M != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-          const float mv = mw[w * 8 + qq];
-          const float f = mv == -INFINITY ? 0.f : ex2(mv - M);
-          const float2 x = ow[(w * 8 + qq) * (D / 2) + (c ^ (qq >> 1 << 2))];
-          O.x = fmaf(f, x.x, O.x);
-          O.y = fmaf(f, x.y, O.y);
-          Ls = fmaf(f, lw[w * 8 + qq], Ls);
+          for (int w = 0; w < WARPS; ++w) {
+            const float mv = mw[w * 8 + qq];
+            const float f = mv == -INFINITY ? 0.f : ex2(mv - M);
+            const float2 x = ow[(w * 8 + qq) * (D / 2) + (c ^ (qq >> 1 << 2))];
+            O.x = fmaf(f, x.x, O.x);
+            O.y = fmaf(f, x.y, O.y);
+            Ls = fmaf(f, lw[w * 8 + qq], Ls);
+          }
         }
+        put(qq, c, O, M, Ls);
       }
-      const int64_t at = int64_t(it.part_base) + qq;
-      reinterpret_cast<float2*>(m.part_o + at * D)[c] = O;
-      if (c == 0) m.part_ml[at] = make_float2(M, Ls);
-    }
+    };
+    if (it.part_base < 0)
+      merge([&](int qq, int c, float2 O, float M, float Ls) {
+        put_out<T, D>(m, out, it, Hq, G, qq, c, O, M, Ls);
+      });
+    else
+      merge([&](int qq, int c, float2 O, float M, float Ls) {
+        const int64_t at = int64_t(it.part_base) + qq;
+        reinterpret_cast<float2*>(m.part_o + at * D)[c] = O;
+        if (c == 0) m.part_ml[at] = make_float2(M, Ls);
+      });
     // the held stage back to the producer (generic writes into a buffer that the
     // copy engine rewrites next)
     fence_proxy_async_smem();
@@ -1019,41 +1067,47 @@ struct KvMaps {
 
 template <typename T, int D, bool WIDE>
 static cudaError_t launch_a8(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_scale,
-                             const uint8_t* v_scale, const uint32_t* mask_words, uint32_t* status,
-                             const KvMaps& maps, cudaStream_t s) {
+                             const uint8_t* v_scale, const uint32_t* mask_words, a8::Outs<T> out,
+                             uint32_t* status, const KvMaps& maps, cudaStream_t s) {
   const int n = WIDE ? p.num_wide_items : p.num_dec_items;
   if (n == 0) return cudaSuccess;
   constexpr bool SPLIT = sizeof(T) == 4;
   constexpr int smem = WIDE ? a8::WideCfg<D, SPLIT>::SMEM : a8::NarrowCfg<D, SPLIT>::SMEM;
   static_assert(smem + 1024 <= 227 * 1024 / 2, "two CTAs per SM at least");
-  auto kernel = WIDE ? attend_kv8_wide_kernel<T, D> : attend_kv8_kernel<T, D>;
   static std::atomic<uint64_t> configured{0};  // per instantiation and device
-  cudaError_t e = set_smem_limit(kernel, smem, configured);
-  if (e != cudaSuccess) return e;
   DevMeta m = p.dev;
   test_wait_hook(&m.test_stall, &m.test_wait_us);
   const int per_sm = std::min(3, 227 * 1024 / (smem + 1024));
   const int grid = std::min(n, per_sm * std::max(1, p.dev.num_sms));
-  return launch_dependent(kernel, dim3(grid), dim3(a8::THREADS), smem, s, true, m,
-                          p.desc.num_q_heads, p.desc.num_kv_heads, p.G, p.desc.page_size,
-                          p.desc.sm_scale * a8::kLog2e, static_cast<const T*>(q_rot), k_scale, v_scale,
-                          mask_words, WIDE ? m.wide_items : m.dec_items, n,
-                          m.dec_work + (WIDE ? 2 : 0), status, maps.k, maps.v);
+  auto launch = [&](auto kernel, auto... outs) {
+    cudaError_t e = set_smem_limit(kernel, smem, configured);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(grid), dim3(a8::THREADS), smem, s, true, m,
+                            p.desc.num_q_heads, p.desc.num_kv_heads, p.G, p.desc.page_size,
+                            p.desc.sm_scale * a8::kLog2e, static_cast<const T*>(q_rot), k_scale, v_scale,
+                            mask_words, WIDE ? m.wide_items : m.dec_items, n,
+                            m.dec_work + (WIDE ? 2 : 0), status, maps.k, maps.v, outs...);
+  };
+  if constexpr (WIDE) return launch(attend_kv8_wide_kernel<T, D>);
+  else return launch(attend_kv8_kernel<T, D>, out);
 }
 
 template <typename T, int D>
 static cudaError_t launch_a8_both(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_scale,
                                   const uint8_t* v_scale, const uint32_t* mask_words,
+                                  void* out_readout, float* lse_readout, void* out_all, float* lse_all,
                                   uint32_t* status, const KvMaps& maps, cudaStream_t s) {
-  cudaError_t e = launch_a8<T, D, false>(p, q_rot, k_scale, v_scale, mask_words, status, maps, s);
+  const a8::Outs<T> out{static_cast<T*>(out_readout), lse_readout, static_cast<T*>(out_all), lse_all};
+  cudaError_t e = launch_a8<T, D, false>(p, q_rot, k_scale, v_scale, mask_words, out, status, maps, s);
   if (e == cudaSuccess)
-    e = launch_a8<T, D, true>(p, q_rot, k_scale, v_scale, mask_words, status, maps, s);
+    e = launch_a8<T, D, true>(p, q_rot, k_scale, v_scale, mask_words, out, status, maps, s);
   return e;
 }
 
 cudaError_t launch_attend_kv8(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_pool,
                               const uint8_t* v_pool, const uint8_t* k_scale,
                               const uint8_t* v_scale, const uint32_t* mask_words,
+                              void* out_readout, float* lse_readout, void* out_all, float* lse_all,
                               uint32_t* status, cudaStream_t s) {
   const int D = p.desc.head_dim, P = p.desc.page_size;
   KvMaps maps;
@@ -1068,7 +1122,8 @@ cudaError_t launch_attend_kv8(const pie_fwd_plan_t& p, const void* q_rot, const 
   const bool bf = p.desc.dtype == PIE_BF16;
   auto f = D == 128 ? (bf ? launch_a8_both<__nv_bfloat16, 128> : launch_a8_both<float, 128>)
                     : (bf ? launch_a8_both<__nv_bfloat16, 64> : launch_a8_both<float, 64>);
-  return f(p, q_rot, k_scale, v_scale, mask_words, status, maps, s);
+  return f(p, q_rot, k_scale, v_scale, mask_words, out_readout, lse_readout, out_all, lse_all, status,
+           maps, s);
 }
 
 }  // namespace pie

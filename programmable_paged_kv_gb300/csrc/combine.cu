@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(128) combine_kernel(DevMeta m, int Hq, int Hkv
   grid_dep_wait();  // the attention kernels' partial states
   grid_dep_launch();
   if (!tables_early) read_tables();
-  if (!active || ce.nchunks < 0) return;  // < 0: written directly by the tensor-core kernel
+  if (!active || ce.nchunks < 0) return;  // < 0: written directly by the attention kernel
   const int qi = (row - ce.row0) * G + h % G;
   // a masked block uses as many chunks as its list length gives, for as many
   // waves of items as its kernel's (one on the tensor-core path, three on the

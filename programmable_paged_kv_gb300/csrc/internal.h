@@ -23,7 +23,9 @@ namespace pie {
 // the sink pages, then the pages from the window's first on -- and `block` is
 // -1 - (the pages left out between them); window_pages() below decodes it.  In
 // passes over 8-bit caches `lane` (of a TcItem too) is where the lane's page-table
-// entries begin in page_ids: one load less before an item's first copy.
+// entries begin in page_ids (one load less before an item's first copy), and
+// part_base is -1 for an item that covers its rows' whole range and writes their
+// outputs.
 struct alignas(16) DecItem {
   int32_t lane, kv_head, row0, nrows;
   int32_t kv_begin, kv_end, part_base, block;
@@ -62,7 +64,7 @@ struct alignas(16) WriteBlock {
 // How the combine step finds the partials of a row block (the rows one work
 // item serves) and kv head: row r of the block, q head h, chunk c lives at
 // part_base + c * stride + (r - row0) * G + (h % G).  nchunks < 0 marks blocks
-// whose outputs the tensor-core kernel wrote directly (nothing to combine).
+// whose outputs the attention kernel wrote directly (nothing to combine).
 // mblock >= 0 marks a masked row block: nchunks is then only the chunks
 // provisioned, and the chunks used come from its list length (masked_chunks
 // for `waves` waves of items: 1 on the tensor-core path, kDecListWaves on the
@@ -259,6 +261,7 @@ cudaError_t launch_append_kv8(const pie_fwd_plan_t& p, const void* q, const void
 cudaError_t launch_attend_kv8(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_pool,
                               const uint8_t* v_pool, const uint8_t* k_scale,
                               const uint8_t* v_scale, const uint32_t* mask_words,
+                              void* out_readout, float* lse_readout, void* out_all, float* lse_all,
                               uint32_t* status, cudaStream_t s);
 cudaError_t launch_attend_kv8_tc(const pie_fwd_plan_t& p, const void* q_rot, const uint8_t* k_pool,
                                  const uint8_t* v_pool, const uint8_t* k_scale,

@@ -442,18 +442,26 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
     work += slots * Hkv;
   }
   int CH = choose_chunk(work);
+  bool one_chunk = false;  // 8-bit caches: every split-KV item covers its rows' whole range
   // 8-bit caches and windows: where that gives less than about four waves of the
   // three CTAs per SM, the chunk that makes the waves' time shortest, an item costing
   // its slots and about kItemSlots more (its first copies, its partials).  (Without
   // and with: 8 windowed lanes of 4,100 slots 36 and 31 us, 33 of 1,033 8-bit
-  // slots 15.5 and 12.4, the 64-lane decode batch 58 either way.)
+  // slots 15.5 and 12.4, the 64-lane decode batch 58 either way.)  Where every item of
+  // an 8-bit cache covers its rows' whole range, the items write the outputs and no
+  // combine step follows, which is worth about kCombineSlots: one row of 300 slots
+  // 11.6 us in three chunks and 9.8 in one, 40 of up to 100 11.3 and 9.7; with 1,024,
+  // 33 rows of 1,033 slots went from 12.4 to 16.  (Not with wide items: the outputs'
+  // code in that kernel cost 48 drafts 166 to 174 us.)
   if (H.kv8 || H.window > 0) {
-    const int kItemSlots = 192;
+    const int kItemSlots = 192, kCombineSlots = 256;
     static thread_local std::vector<int32_t> exts;
     exts.clear();
     int longest = 1;
+    bool any_wide = false;
     for (int l = 0; l < L; ++l) {
       if (lane_tc(l)) continue;
+      any_wide = any_wide || lane_wide(l);
       const int r0 = M.row_indptr[l], r1 = M.row_indptr[l + 1];
       const int rows = lane_wide(l) ? wide_rows : rows_per_item;
       for (int b0 = r0; b0 < r1; b0 += rows) {
@@ -475,11 +483,14 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
         if (items == 0) break;
         if (items > 4 * cap) continue;
         const double mean = static_cast<double>(work) / items + kItemSlots;
-        const double cost = static_cast<double>((items + cap - 1) / cap) * mean;
+        double cost = static_cast<double>((items + cap - 1) / cap) * mean;
+        if (items <= cap) cost = static_cast<double>(std::min<int64_t>(ch, longest) + kItemSlots);
+        if (ch < longest || !H.kv8 || any_wide) cost += kCombineSlots;
         if (best < 0.0 || cost < best) best = cost, CH = static_cast<int>(ch);
         if (ch >= longest) break;
       }
     }
+    one_chunk = H.kv8 && CH >= longest && !any_wide;
   }
   // tensor-core items: two query tiles per item when some lane has more than
   // 128 query vectors per kv head (they then share every K/V tile)
@@ -614,12 +625,12 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
       } else {
         // a listed unit has at least one item: the combine step reads at
         // least one chunk of every list (an empty list's item writes the
-        // empty state)
+        // empty state); an 8-bit cache's only item writes its rows' outputs itself
         nchunks = (ext + CH - 1) / CH;
-        if (!block_of_row.empty() && block_of_row[b0] >= 0) nchunks = std::max(1, nchunks);
+        if (one_chunk || (!block_of_row.empty() && block_of_row[b0] >= 0)) nchunks = std::max(1, nchunks);
         chunk = CH;
       }
-      const bool direct = use_tc && nchunks == 1;
+      const bool direct = use_tc ? nchunks == 1 : one_chunk;
       const int32_t mblk = block_of_row.empty() ? -1 : block_of_row[b0];
       for (int g = 0; g < Hkv; ++g) {
         H.comb.push_back(CombEntry{static_cast<int32_t>(part), direct ? -1 : nchunks,
@@ -642,11 +653,11 @@ static int build_host_plan(const pie_fwd_desc* desc, const pie_fwd_cache* cache,
           DecItem* di = items.data() + base;
           for (int c = 0; c < nchunks; ++c) {
             const int kb = c * chunk;
-            const int32_t pb = static_cast<int32_t>(part + int64_t(c) * stride);
+            const int32_t pb = direct ? -1 : static_cast<int32_t>(part + int64_t(c) * stride);
             di[c] = mblk >= 0 ? DecItem{l, g, b0, b1 - b0, c, nchunks, pb, mblk}
                               : DecItem{item_lane, g, b0, b1 - b0, kb, std::min(ext, kb + chunk), pb, -1 - skip};
           }
-          part += int64_t(nchunks) * stride;
+          part += direct ? 0 : int64_t(nchunks) * stride;
         }
       }
     }
@@ -1043,7 +1054,8 @@ int pie_fwd_attend_kv8(const pie_fwd_plan_t* plan, const void* q_rot, const uint
   cudaError_t e = cudaSuccess;
   if (g_ev_start) e = cudaEventRecord(g_ev_start, s);
   if (e == cudaSuccess && plan->num_dec_items + plan->num_wide_items > 0)
-    e = launch_attend_kv8(*plan, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words, status, s);
+    e = launch_attend_kv8(*plan, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words, out_readout,
+                          lse_readout, out_all, lse_all, status, s);
   if (e == cudaSuccess && plan->num_tc_items > 0)
     e = launch_attend_kv8_tc(*plan, q_rot, k_pool, v_pool, k_scale, v_scale, mask_words,
                              out_readout, lse_readout, out_all, lse_all, status, s);

@@ -526,3 +526,27 @@ def test_too_few_mask_words_and_too_many_pages_are_refused():
 def test_attend_sinks_past_every_slot(desc):
     p, pages = CC.make_pass(97, desc, [CC.tail(400, 1), CC.tail(70, 6), CC.tail(333, 30)])
     _check_attend(desc, p, pages, 98, 5, 2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("kv", [40, 3000], ids=["one chunk", "chunks"])
+@pytest.mark.parametrize("rows", [1, 8], ids=["narrow", "wide"])
+@pytest.mark.parametrize("desc", DESCS[:3], ids=str)
+def test_outputs_asked_for_one_by_one(desc, rows, kv):
+    """Every subset of the outputs is the same bits as all of them, rows that are read
+    out twice or not at all included, and nothing else is written."""
+    lanes = [CC.tail(kv, rows), (0, list(range(rows)))]
+    p, pages, (q, _, _), pool = _state(99, desc, lanes)
+    p.readout = np.array([0, 2 * rows - 1, 0], np.int32)
+    plan = CC.plan_of(desc, p, pages, kv="e4m3")
+    shapes = [(3, *q.shape[1:]), (3, q.shape[1]), tuple(q.shape), tuple(q.shape[:2])]
+    new = lambda: [torch.full(s, 7.0, dtype=q.dtype if len(s) == 3 else torch.float32, device="cuda")
+                   for s in shapes]
+    want = new()
+    plan.attend_kv8(q, *pool, None, *want)
+    for pick in ((0,), (2,), (0, 1), (2, 3), (0, 3), (1, 2)):
+        got = new()
+        plan.attend_kv8(q, *pool, None, *(x if i in pick else None for i, x in enumerate(got)))
+        for i in range(4):
+            assert torch.equal(got[i], want[i] if i in pick else torch.full_like(got[i], 7.0))
+    assert torch.equal(want[0], want[2][p.readout.tolist()]) and torch.equal(want[1], want[3][p.readout.tolist()])
+    plan.close()
