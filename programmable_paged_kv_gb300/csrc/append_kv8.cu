@@ -44,6 +44,9 @@ namespace ak {
 constexpr int WARPS = 8, THREADS = 32 * WARPS;
 constexpr int QUNITS = 128;  // (row, query head) units per query CTA
 
+// as many as the registers of a warp's rows leave room for
+constexpr int ctas_per_sm(int row_bytes) { return row_bytes <= 32 ? 3 : row_bytes <= 64 ? 2 : 1; }
+
 // cos and sin of 2 pi t / 2^64, each as a sum of two floats
 struct Angle {
   float ch, cl, sh, sl;
@@ -218,7 +221,7 @@ __device__ __forceinline__ int settle(int ex, uint8_t* codes, uint8_t* scale, ui
 // (prompts 8 x 512 at 16 slots a page: 22 us with 16, 27 with 32; a decode step 9.6
 // either way).
 template <typename T, int D, int MAXR>
-__global__ void __launch_bounds__(ak::THREADS, sizeof(T) * MAXR <= 32 ? 3 : sizeof(T) * MAXR <= 64 ? 2 : 1) append_kv8_kernel(
+__global__ void __launch_bounds__(ak::THREADS, ak::ctas_per_sm(sizeof(T) * MAXR)) append_kv8_kernel(
     DevMeta m, int Hq, int Hkv, int P, int head_ctas, const T* q, const T* k, const T* v, T* q_rot,
     uint8_t* k_pool, uint8_t* v_pool, uint8_t* k_scale, uint8_t* v_scale,
     const int32_t* frozen_len, uint32_t* status) {

@@ -442,7 +442,9 @@ __global__ void __launch_bounds__(tc::Cfg<NT>::kThreads, 1) attend_tc_kernel(
           for (int c = 0; c < BN; ++c) {
             const int sa = ts + c;
             const bool vis = valid_q && sa < ke &&
-                             (WIN ? view.sees(row_slot, view.slot(sa)) : masked ? ((words[c >> 5] >> (c & 31)) & 1u) != 0 : sa <= row_slot);
+                             (WIN      ? view.sees(row_slot, view.slot(sa))
+                              : masked ? ((words[c >> 5] >> (c & 31)) & 1u) != 0
+                                       : sa <= row_slot);
             s[c] = vis ? s[c] : -INFINITY;
           }
         }
